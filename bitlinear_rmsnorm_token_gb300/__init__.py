@@ -20,6 +20,8 @@ __all__ = [
     "FLAG_WEIGHTS_STATIC", "MAX_GROUP", "EXPORTED_FUNCTIONS", "bitlinear_forward_noalloc",
     "selftest_bounded_wait", "glu", "glu_rmsnorm_quant_a8", "bitlinear_forward_glu", "ACT_SILU", "ACT_GELU_TANH",
     "bitlinear_forward_typed", "DTYPE_F32", "DTYPE_F16", "DTYPE_BF16", "head_rmsnorm", "bitlinear_forward_qk",
+    "quant_w8", "w8a8_gemm", "w8a8_forward", "KV4_PAGE", "kv4_block_bytes", "kv4_cache", "kv4_append", "kv4_read",
+    "kv4_attention",
 ]
 
 OK = 0
@@ -30,6 +32,8 @@ ERR_CUDA = 4
 ERR_TIMEOUT = 5
 ERR_NO_DEVICE = 6
 ERR_SCRATCH_LIMIT = 7
+ERR_BAD_INDEX = 8
+KV4_PAGE = 64
 NOALLOC_SCRATCH_BYTES = 16 << 20
 FLAG_WEIGHTS_STATIC = 1
 MAX_GROUP = 16
@@ -45,6 +49,8 @@ EXPORTED_FUNCTIONS = (
     "bitnet_status_string", "bitnet_last_device_status", "bitnet_bitlinear_forward_noalloc",
     "bitnet_selftest_bounded_wait", "bitnet_glu", "bitnet_glu_rmsnorm_quant_a8", "bitnet_bitlinear_forward_glu",
     "bitnet_bitlinear_forward_typed", "bitnet_head_rmsnorm", "bitnet_bitlinear_forward_qk",
+    "bitnet_quant_w8", "bitnet_w8a8_gemm", "bitnet_w8a8_forward", "bitnet_kv4_cache_bytes", "bitnet_kv4_append",
+    "bitnet_kv4_read", "bitnet_kv4_attention",
 )
 
 
@@ -59,6 +65,15 @@ class Projection(ctypes.Structure):
     _fields_ = [
         ("x", ctypes.c_void_p), ("norm_w", ctypes.c_void_p), ("packed_w", ctypes.c_void_p),
         ("w_scale", ctypes.c_float), ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("y", ctypes.c_void_p),
+    ]
+
+
+class Kv4(ctypes.Structure):
+    """Mirror of bitnet_kv4."""
+    _fields_ = [
+        ("cache", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("q_start", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p), ("num_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
     ]
 
 
@@ -110,6 +125,22 @@ def lib(build: bool = False) -> ctypes.CDLL:
     L.bitnet_bitlinear_forward_typed.restype = ctypes.c_int
     L.bitnet_bitlinear_forward_typed.argtypes = [vp, ctypes.c_int, vp, ctypes.c_int, vp, f32, i64, i64, i64, f32, vp,
                                                  ctypes.c_int, vp]
+    L.bitnet_quant_w8.restype = ctypes.c_int
+    L.bitnet_quant_w8.argtypes = [vp, i64, i64, vp, vp, vp]
+    L.bitnet_w8a8_gemm.restype = ctypes.c_int
+    L.bitnet_w8a8_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, ctypes.c_int, vp, vp]
+    L.bitnet_w8a8_forward.restype = ctypes.c_int
+    L.bitnet_w8a8_forward.argtypes = [vp, ctypes.c_int, vp, vp, vp, i64, i64, i64, f32, vp, ctypes.c_int, vp]
+    L.bitnet_kv4_cache_bytes.restype = ctypes.c_size_t
+    L.bitnet_kv4_cache_bytes.argtypes = [i64, i32, i32]
+    kv = ctypes.POINTER(Kv4)
+    L.bitnet_kv4_append.restype = ctypes.c_int
+    L.bitnet_kv4_append.argtypes = [kv, vp, vp, ctypes.c_int, i64, vp]
+    L.bitnet_kv4_read.restype = ctypes.c_int
+    L.bitnet_kv4_read.argtypes = [kv, i64, vp, vp, ctypes.c_int, vp]
+    L.bitnet_kv4_attention.restype = ctypes.c_int
+    L.bitnet_kv4_attention.argtypes = [kv, vp, ctypes.c_int, i64, i32, i32, f32, ctypes.c_int, i32, vp, ctypes.c_int,
+                                       vp]
     _lib = L
     return L
 
@@ -381,6 +412,185 @@ def bitlinear_forward_group(group, M: int, eps: float = 1e-6, flags: int = 0, st
         group = make_group(group)
     rc = lib().bitnet_bitlinear_forward_group(group, len(group), int(M), float(eps), int(flags), _stream(stream))
     _check(rc, "bitnet_bitlinear_forward_group")
+
+
+def _on_current_device(where, *tensors):
+    """The kernels run on the current device: tensors of another one are refused."""
+    import torch
+
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise ValueError(f"{where}: a tensor is on {t.device}, the current device is cuda:{here}")
+
+
+def _shape(where, name, t, want):
+    if tuple(t.shape) != tuple(want):
+        raise ValueError(f"{where}: {name} must have the shape {tuple(want)}, got {tuple(t.shape)}")
+
+
+def quant_w8(w, codes=None, scale=None, stream=None):
+    """Absmax int8 quantisation of w[N, K] (fp32), one scale per row.  Returns
+    (codes int8 [N, K], scale f32 [N]), scale = 127 / max|row|."""
+    import torch
+
+    N, K = w.shape
+    if codes is None:
+        codes = torch.empty((N, K), dtype=torch.int8, device=w.device)
+    if scale is None:
+        scale = torch.empty(N, dtype=torch.float32, device=w.device)
+    _shape("quant_w8", "codes", codes, (N, K))
+    _shape("quant_w8", "scale", scale, (N,))
+    args = (_dev(w, torch.float32, "w"), N, K, _dev(codes, torch.int8, "codes"),
+            _dev(scale, torch.float32, "scale"))
+    _on_current_device("quant_w8", w, codes, scale)
+    _check(lib().bitnet_quant_w8(*args, _stream(stream)), "bitnet_quant_w8")
+    return codes, scale
+
+
+_ANY_DTYPE = (DTYPE_F32, DTYPE_F16, DTYPE_BF16)
+
+
+def w8a8_gemm(codes, a_scale, w_codes, w_scale, y=None, y_dtype=None, acc_out=None, stream=None):
+    """y[M, N] = (codes . w_codes^T) / a_scale[:, None] / w_scale: int8 codes of
+    rmsnorm_quant_a8 and quant_w8; y float32 (default), float16 or bfloat16."""
+    import torch
+
+    M, K = codes.shape
+    N = w_codes.shape[0]
+    if y is None:
+        y = torch.empty((M, N), dtype=y_dtype if y_dtype is not None else torch.float32, device=codes.device)
+    _shape("w8a8_gemm", "a_scale", a_scale, (M,))
+    _shape("w8a8_gemm", "w_codes", w_codes, (N, K))
+    _shape("w8a8_gemm", "w_scale", w_scale, (N,))
+    _shape("w8a8_gemm", "y", y, (M, N))
+    if acc_out is not None:
+        _shape("w8a8_gemm", "acc_out", acc_out, (M, N))
+    yt = _dtype_code(y, "y", _ANY_DTYPE)
+    args = (_dev(codes, torch.int8, "codes"), _dev(a_scale, torch.float32, "a_scale"),
+            _dev(w_codes, torch.int8, "w_codes"), _dev(w_scale, torch.float32, "w_scale"), M, K, N,
+            _dev(y, y.dtype, "y"), yt, _opt(acc_out, torch.int32, "acc_out"))
+    _on_current_device("w8a8_gemm", codes, a_scale, w_codes, w_scale, y, acc_out)
+    _check(lib().bitnet_w8a8_gemm(*args, _stream(stream)), "bitnet_w8a8_gemm")
+    return y
+
+
+def w8a8_forward(x, norm_w, w_codes, w_scale, eps: float = 1e-6, y=None, y_dtype=None, stream=None):
+    """The projection with 8-bit weights: RMSNorm of x[M, K] (float32, float16 or
+    bfloat16) with norm_w, per-token int8 quantisation, w8a8_gemm.  y in y_dtype
+    (default: x's dtype)."""
+    import torch
+
+    M, K = x.shape
+    N = w_codes.shape[0]
+    if y is None:
+        y = torch.empty((M, N), dtype=y_dtype if y_dtype is not None else x.dtype, device=x.device)
+    _shape("w8a8_forward", "norm_w", norm_w, (K,))
+    _shape("w8a8_forward", "w_codes", w_codes, (N, K))
+    _shape("w8a8_forward", "w_scale", w_scale, (N,))
+    _shape("w8a8_forward", "y", y, (M, N))
+    xt = _dtype_code(x, "x", _ANY_DTYPE)
+    yt = _dtype_code(y, "y", _ANY_DTYPE)
+    args = (_dev(x, x.dtype, "x"), xt, _dev(norm_w, torch.float32, "norm_w"), _dev(w_codes, torch.int8, "w_codes"),
+            _dev(w_scale, torch.float32, "w_scale"), M, K, N, float(eps), _dev(y, y.dtype, "y"), yt)
+    _on_current_device("w8a8_forward", x, norm_w, w_codes, w_scale, y)
+    _check(lib().bitnet_w8a8_forward(*args, _stream(stream)), "bitnet_w8a8_forward")
+    return y
+
+
+def kv4_block_bytes(head_dim: int) -> int:
+    """Bytes of one page of one kv head (KV4_PAGE tokens, keys and values)."""
+    n = int(lib().bitnet_kv4_cache_bytes(1, 1, head_dim))
+    if n == 0:
+        raise BitnetError(ERR_UNSUPPORTED_SHAPE, "kv4_block_bytes")
+    return n
+
+
+def kv4_cache(num_pages: int, num_kv_heads: int, head_dim: int, device="cuda"):
+    """A 4-bit key/value cache: uint8 [num_pages, num_kv_heads, kv4_block_bytes(head_dim)], uninitialised."""
+    import torch
+
+    return torch.empty((num_pages, num_kv_heads, kv4_block_bytes(head_dim)), dtype=torch.uint8, device=device)
+
+
+def _kv4(where, cache, num_kv_heads, head_dim, q_start, kv_lens, page_table):
+    import torch
+
+    if page_table.dim() != 2:
+        raise ValueError(f"{where}: page_table must be [sequences, pages]")
+    B, most = page_table.shape
+    _shape(where, "q_start", q_start, (B + 1,))
+    _shape(where, "kv_lens", kv_lens, (B,))
+    if cache.dim() != 3 or cache.shape[1] != num_kv_heads or cache.shape[2] != 64 * head_dim + 16 * KV4_PAGE:
+        raise ValueError(f"{where}: cache must be [pages, {num_kv_heads}, {64 * head_dim + 16 * KV4_PAGE}], "
+                         f"got {tuple(cache.shape)}")
+    return Kv4(_dev(cache, torch.uint8, "cache"), cache.shape[0], num_kv_heads, head_dim,
+               _dev(q_start, torch.int32, "q_start"), _dev(kv_lens, torch.int32, "kv_lens"),
+               _dev(page_table, torch.int32, "page_table"), B, most)
+
+
+def kv4_append(k, v, cache, q_start, kv_lens, page_table, stream=None):
+    """Quantises the rows k, v [T, kv heads, D] (float32, float16 or bfloat16; D 128 or 256) into the 4-bit cache.
+
+    Sequence b owns rows q_start[b] .. q_start[b + 1] - 1, its last tokens: row i of n is position kv_lens[b] - n + i
+    (kv_lens counts them), kept in page page_table[b, position // KV4_PAGE].  int32 arrays on the device."""
+    T, H, D = k.shape
+    _shape("kv4_append", "v", v, k.shape)
+    if v.dtype != k.dtype:
+        raise TypeError("kv4_append: k and v differ in dtype")
+    t = _dtype_code(k, "k", _ANY_DTYPE)
+    c = _kv4("kv4_append", cache, H, D, q_start, kv_lens, page_table)
+    args = (_dev(k, k.dtype, "k"), _dev(v, v.dtype, "v"), t, T)
+    _on_current_device("kv4_append", k, v, cache, q_start, kv_lens, page_table)
+    _check(lib().bitnet_kv4_append(ctypes.byref(c), *args, _stream(stream)), "bitnet_kv4_append")
+
+
+def kv4_read(cache, T: int, num_kv_heads: int, head_dim: int, q_start, kv_lens, page_table, dtype=None, k=None, v=None,
+             stream=None):
+    """The plan's rows as the values that the cache holds: (k, v) [T, kv heads, D] in dtype (default float32).  Rows
+    of no sequence are left as they are."""
+    import torch
+
+    shape = (T, num_kv_heads, head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype or (torch.float32 if v is None else v.dtype), device=cache.device)
+    if v is None:
+        v = torch.empty(shape, dtype=k.dtype, device=cache.device)
+    _shape("kv4_read", "k", k, shape)
+    _shape("kv4_read", "v", v, shape)
+    if v.dtype != k.dtype or (dtype is not None and k.dtype != dtype):
+        raise TypeError("kv4_read: k, v and dtype differ")
+    t = _dtype_code(k, "k", _ANY_DTYPE)
+    c = _kv4("kv4_read", cache, num_kv_heads, head_dim, q_start, kv_lens, page_table)
+    args = (T, _dev(k, k.dtype, "k"), _dev(v, v.dtype, "v"), t)
+    _on_current_device("kv4_read", k, v, cache, q_start, kv_lens, page_table)
+    _check(lib().bitnet_kv4_read(ctypes.byref(c), *args, _stream(stream)), "bitnet_kv4_read")
+    return k, v
+
+
+def kv4_attention(q, cache, num_kv_heads: int, q_start, kv_lens, page_table, max_q_len: int, scale: float = None,
+                  causal: bool = True, window: int = 0, out=None, out_dtype=None, stream=None):
+    """Softmax attention of q [T, heads, D] over the 4-bit cache; out [T, heads, D] in q's dtype or float32.
+
+    Rows belong to sequences as in kv4_append.  A row at position p sees the keys j <= p (causal), of them the last
+    `window` where window > 0, or all kv_lens[b] keys (causal=False); a row that sees none gives zeros.  max_q_len
+    bounds the sequences' row counts; scale defaults to 1 / sqrt(D)."""
+    import torch
+
+    T, Hq, D = q.shape
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype if out_dtype is not None else q.dtype, device=q.device)
+    _shape("kv4_attention", "out", out, q.shape)
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError("kv4_attention: out and out_dtype differ")
+    qt = _dtype_code(q, "q", _ANY_DTYPE)
+    ot = _dtype_code(out, "out", (qt, DTYPE_F32))
+    c = _kv4("kv4_attention", cache, num_kv_heads, D, q_start, kv_lens, page_table)
+    args = (_dev(q, q.dtype, "q"), qt, T, Hq, int(max_q_len), D ** -0.5 if scale is None else float(scale),
+            1 if causal else 0, int(window), _dev(out, out.dtype, "out"), ot)
+    _on_current_device("kv4_attention", q, cache, q_start, kv_lens, page_table, out)
+    _check(lib().bitnet_kv4_attention(ctypes.byref(c), *args, _stream(stream)), "bitnet_kv4_attention")
+    return out
 
 
 def last_device_status(stream=None) -> int:

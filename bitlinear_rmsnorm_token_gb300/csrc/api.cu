@@ -142,6 +142,8 @@ const char* bitnet_status_string(int status) {
     case BITNET_ERR_NO_DEVICE: return "no sm_103 CUDA device";
     case BITNET_ERR_SCRATCH_LIMIT:
       return "problem needs more than the 16 MiB no-alloc scratch (2*M*K + 4*M bytes); use bitnet_bitlinear_forward";
+    case BITNET_ERR_BAD_INDEX:
+      return "a cache plan held an index out of range (see bitnet_last_device_status)";
     default: return "unknown status";
   }
 }
@@ -619,7 +621,7 @@ int bitnet_last_device_status(bitnet_stream_t stream) {
   if (cudaMemcpy(&word, ctx->err_word, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return BITNET_ERR_CUDA;
   if (word == 0) return BITNET_OK;
   if (cudaMemset(ctx->err_word, 0, sizeof(unsigned)) != cudaSuccess) return BITNET_ERR_CUDA;
-  return BITNET_ERR_TIMEOUT;
+  return (word & kErrWaitTimeout) ? BITNET_ERR_TIMEOUT : BITNET_ERR_BAD_INDEX;
 }
 
 }  // extern "C"

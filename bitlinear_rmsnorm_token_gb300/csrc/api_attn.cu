@@ -1,0 +1,146 @@
+// api_attn.cu -- C ABI of the 8-bit projections and of the 4-bit key/value
+// cache: argument checks and dispatch.
+#include <cmath>
+
+#include "common.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+
+namespace bitnet {
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool known_dtype(int t) { return t == BITNET_DTYPE_F32 || t == BITNET_DTYPE_F16 || t == BITNET_DTYPE_BF16; }
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? BITNET_OK : BITNET_ERR_CUDA; }
+
+constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
+
+int check_w8_shape(int64_t M, int64_t K, int64_t N) {
+  if (M < 1 || N < 1) return BITNET_ERR_INVALID_ARG;
+  if (K < 128 || K % 128 != 0 || K > BITNET_MAX_K) return BITNET_ERR_UNSUPPORTED_SHAPE;
+  if (M > kMaxInt || N > kMaxInt) return BITNET_ERR_UNSUPPORTED_SHAPE;
+  return BITNET_OK;
+}
+
+// Checks a cache descriptor and T, and turns it into what the kernels take.
+int check_kv4(const bitnet_kv4* c, int64_t T, KvView* v) {
+  if (!c || !c->cache || !c->q_start || !c->kv_lens || !c->page_table) return BITNET_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->num_kv_heads < 1 || c->num_seqs < 1 || c->max_pages < 1 || T < 1)
+    return BITNET_ERR_INVALID_ARG;
+  if (c->head_dim != 128 && c->head_dim != 256) return BITNET_ERR_UNSUPPORTED_SHAPE;
+  // positions, rows and page indices are 32-bit on the device
+  if (c->num_pages > kMaxInt || T > kMaxInt || c->max_pages > kMaxInt / BITNET_KV4_PAGE || c->num_kv_heads > 65535)
+    return BITNET_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(c->cache) || !aligned4(c->q_start) || !aligned4(c->kv_lens) || !aligned4(c->page_table))
+    return BITNET_ERR_MISALIGNED;
+  *v = KvView{static_cast<uint8_t*>(c->cache), c->q_start, c->kv_lens, c->page_table, c->num_pages,
+              c->num_seqs,                     c->max_pages, c->num_kv_heads};
+  return BITNET_OK;
+}
+
+}  // namespace
+}  // namespace bitnet
+
+using namespace bitnet;
+
+extern "C" {
+
+int bitnet_quant_w8(const float* w, int64_t N, int64_t K, int8_t* w_codes, float* w_scale, bitnet_stream_t stream) {
+  if (!w || !w_codes || !w_scale) return BITNET_ERR_INVALID_ARG;
+  int rc = check_w8_shape(1, K, N);
+  if (rc) return rc;
+  if (!aligned16(w) || !aligned16(w_codes) || !aligned4(w_scale)) return BITNET_ERR_MISALIGNED;
+  DeviceContext* ctx;
+  if ((rc = device_context(&ctx))) return rc;
+  return cuda_status(launch_quant_w8(w, N, K, w_codes, w_scale, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bitnet_w8a8_gemm(const int8_t* a_codes, const float* a_scale, const int8_t* w_codes, const float* w_scale,
+                     int64_t M, int64_t K, int64_t N, void* y, int y_dtype, int32_t* acc_out,
+                     bitnet_stream_t stream) {
+  if (!a_codes || !a_scale || !w_codes || !w_scale || !y || !known_dtype(y_dtype)) return BITNET_ERR_INVALID_ARG;
+  int rc = check_w8_shape(M, K, N);
+  if (rc) return rc;
+  if (!aligned16(a_codes) || !aligned4(a_scale) || !aligned16(w_codes) || !aligned4(w_scale) || !aligned16(y) ||
+      (acc_out && !aligned16(acc_out)))
+    return BITNET_ERR_MISALIGNED;
+  DeviceContext* ctx;
+  if ((rc = device_context(&ctx))) return rc;
+  return cuda_status(launch_w8a8(ctx, a_codes, a_scale, w_codes, w_scale, M, K, N, y, y_dtype, acc_out,
+                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bitnet_w8a8_forward(const void* x, int x_dtype, const float* norm_w, const int8_t* w_codes, const float* w_scale,
+                        int64_t M, int64_t K, int64_t N, float eps, void* y, int y_dtype, bitnet_stream_t stream) {
+  if (!x || !norm_w || !w_codes || !w_scale || !y || !known_dtype(x_dtype) || !known_dtype(y_dtype))
+    return BITNET_ERR_INVALID_ARG;
+  if (!(eps > 0.0f)) return BITNET_ERR_INVALID_ARG;
+  int rc = check_w8_shape(M, K, N);
+  if (rc) return rc;
+  if (!aligned16(x) || !aligned16(norm_w) || !aligned16(w_codes) || !aligned4(w_scale) || !aligned16(y))
+    return BITNET_ERR_MISALIGNED;
+  DeviceContext* ctx;
+  if ((rc = device_context(&ctx))) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const size_t code_bytes = (static_cast<size_t>(M * K) + 255) & ~size_t(255);
+  uint8_t* ws = nullptr;
+  if ((rc = pool_alloc(ctx, reinterpret_cast<void**>(&ws), code_bytes + static_cast<size_t>(M) * 4, s))) return rc;
+  int8_t* codes = reinterpret_cast<int8_t*>(ws);
+  float* as = reinterpret_cast<float*>(ws + code_bytes);
+  cudaError_t e = launch_rmsnorm_quant_i8_in(x, x_dtype, norm_w, M, static_cast<int>(K), eps, codes, as, false, s);
+  if (e == cudaSuccess) e = launch_w8a8(ctx, codes, as, w_codes, w_scale, M, K, N, y, y_dtype, nullptr, s);
+  pool_free(ws, s);
+  return cuda_status(e);
+}
+
+size_t bitnet_kv4_cache_bytes(int64_t num_pages, int32_t num_kv_heads, int32_t head_dim) {
+  if (num_pages < 1 || num_kv_heads < 1 || (head_dim != 128 && head_dim != 256)) return 0;
+  return static_cast<size_t>(num_pages) * static_cast<size_t>(num_kv_heads) *
+         (static_cast<size_t>(BITNET_KV4_PAGE) * static_cast<size_t>(head_dim) + 16 * BITNET_KV4_PAGE);
+}
+
+int bitnet_kv4_append(const bitnet_kv4* c, const void* k, const void* v, int dtype, int64_t T,
+                      bitnet_stream_t stream) {
+  KvView view;
+  if (!k || !v || !known_dtype(dtype)) return BITNET_ERR_INVALID_ARG;
+  int rc = check_kv4(c, T, &view);
+  if (rc) return rc;
+  if (!aligned16(k) || !aligned16(v)) return BITNET_ERR_MISALIGNED;
+  DeviceContext* ctx;
+  if ((rc = device_context(&ctx))) return rc;
+  return cuda_status(launch_kv4_append(ctx, view, c->head_dim, k, v, dtype, T,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bitnet_kv4_read(const bitnet_kv4* c, int64_t T, void* k, void* v, int dtype, bitnet_stream_t stream) {
+  KvView view;
+  if (!k || !v || !known_dtype(dtype)) return BITNET_ERR_INVALID_ARG;
+  int rc = check_kv4(c, T, &view);
+  if (rc) return rc;
+  if (!aligned16(k) || !aligned16(v)) return BITNET_ERR_MISALIGNED;
+  DeviceContext* ctx;
+  if ((rc = device_context(&ctx))) return rc;
+  return cuda_status(launch_kv4_read(ctx, view, c->head_dim, k, v, dtype, T, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bitnet_kv4_attention(const bitnet_kv4* c, const void* q, int q_dtype, int64_t T, int32_t num_heads,
+                         int32_t max_q_len, float scale, int causal, int32_t window, void* out, int out_dtype,
+                         bitnet_stream_t stream) {
+  KvView view;
+  if (!q || !out || !known_dtype(q_dtype) || (out_dtype != q_dtype && out_dtype != BITNET_DTYPE_F32))
+    return BITNET_ERR_INVALID_ARG;
+  int rc = check_kv4(c, T, &view);
+  if (rc) return rc;
+  if (num_heads < 1 || num_heads % c->num_kv_heads != 0 || max_q_len < 1 || window < 0 || (causal != 0 && causal != 1) ||
+      (!causal && window != 0) || !std::isfinite(scale))
+    return BITNET_ERR_INVALID_ARG;
+  if (num_heads > 65535) return BITNET_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(q) || !aligned16(out)) return BITNET_ERR_MISALIGNED;
+  DeviceContext* ctx;
+  if ((rc = device_context(&ctx))) return rc;
+  return cuda_status(launch_kv4_attention(ctx, view, c->head_dim, q, q_dtype, T, num_heads, max_q_len, scale, causal,
+                                          window, out, out_dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

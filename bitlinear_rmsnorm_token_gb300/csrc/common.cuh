@@ -14,6 +14,7 @@ namespace bitnet {
 
 // Bits of the per-device error word (see bitnet_last_device_status).
 constexpr unsigned kErrWaitTimeout = 1u;
+constexpr unsigned kErrBadIndex = 2u;  // a cache plan's device-side index was out of range
 
 // A bounded wait gives up after this long.  Correct launches never get close:
 // the longest wait in a healthy kernel is one DRAM/TMA round trip or one tile.

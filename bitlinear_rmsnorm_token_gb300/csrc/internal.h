@@ -159,4 +159,25 @@ cudaError_t launch_gemm_skinny(const DeviceContext* ctx, void* codes, const int3
                                int32_t* acc_out, void* workspace, bool workspace_zeroed, bool pdl, cudaStream_t s,
                                int* status);
 
+// Norm/quant with x in x_dtype and int8 codes (the few-token 8-bit projection).
+cudaError_t launch_rmsnorm_quant_i8_in(const void* x, int x_dtype, const float* g, int64_t M, int K, float eps,
+                                       int8_t* codes, float* a_scale, bool pdl, cudaStream_t s);
+
+// 8-bit weights: per-channel quantisation, and the int8 x int8 contraction on
+// int8 activation codes.
+cudaError_t launch_quant_w8(const float* w, int64_t N, int64_t K, int8_t* codes, float* scale, cudaStream_t s);
+cudaError_t launch_w8a8(DeviceContext* ctx, const int8_t* a, const float* a_scale, const int8_t* w,
+                        const float* w_scale, int64_t M, int64_t K, int64_t N, void* y, int y_dtype, int32_t* acc_out,
+                        cudaStream_t s);
+
+// The paged 4-bit key/value cache (kv4.cuh): head_dim 128 or 256.
+struct KvView;
+cudaError_t launch_kv4_append(const DeviceContext* ctx, const KvView& c, int head_dim, const void* k, const void* v,
+                              int dtype, int64_t T, cudaStream_t s);
+cudaError_t launch_kv4_read(const DeviceContext* ctx, const KvView& c, int head_dim, void* k, void* v, int dtype,
+                            int64_t T, cudaStream_t s);
+cudaError_t launch_kv4_attention(DeviceContext* ctx, const KvView& c, int head_dim, const void* q, int q_dtype,
+                                 int64_t T, int Hq, int max_q_len, float scale, int causal, int window, void* out,
+                                 int out_dtype, cudaStream_t s);
+
 }  // namespace bitnet

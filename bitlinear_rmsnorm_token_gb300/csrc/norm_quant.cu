@@ -432,6 +432,23 @@ cudaError_t launch_rmsnorm_quant_f16_in(const void* x, int x_dtype, const float*
   }
 }
 
+cudaError_t launch_rmsnorm_quant_i8_in(const void* x, int x_dtype, const float* g, int64_t M, int K, float eps,
+                                       int8_t* codes, float* a_scale, bool pdl, cudaStream_t s) {
+  switch (x_dtype) {
+    case BITNET_DTYPE_F32:
+      return launch_nq_k<float, int8_t>(static_cast<const float*>(x), g, M, K, eps, codes, a_scale, nullptr, nullptr,
+                                        pdl, s);
+    case BITNET_DTYPE_F16:
+      return launch_nq_k<__half, int8_t>(static_cast<const __half*>(x), g, M, K, eps, codes, a_scale, nullptr,
+                                         nullptr, pdl, s);
+    case BITNET_DTYPE_BF16:
+      return launch_nq_k<__nv_bfloat16, int8_t>(static_cast<const __nv_bfloat16*>(x), g, M, K, eps, codes, a_scale,
+                                                nullptr, nullptr, pdl, s);
+    default:
+      return cudaErrorInvalidValue;
+  }
+}
+
 cudaError_t launch_rmsnorm_quant_planes(const void* x, int x_dtype, const float* g, int64_t M, int K, float eps,
                                        void* planes, float* a_scale, int32_t* rowsum, bool pdl, cudaStream_t s) {
   PlaneCode* out = static_cast<PlaneCode*>(planes);

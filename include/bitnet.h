@@ -90,7 +90,8 @@ typedef enum {
   BITNET_ERR_CUDA = 4,              /* a CUDA runtime call or launch failed                */
   BITNET_ERR_TIMEOUT = 5,           /* a device-side bounded wait expired (see last_device_status) */
   BITNET_ERR_NO_DEVICE = 6,         /* no CUDA device, or it is not sm_103                 */
-  BITNET_ERR_SCRATCH_LIMIT = 7      /* too large for bitnet_bitlinear_forward_noalloc      */
+  BITNET_ERR_SCRATCH_LIMIT = 7,     /* too large for bitnet_bitlinear_forward_noalloc      */
+  BITNET_ERR_BAD_INDEX = 8          /* a cache plan's device-side index was out of range (see last_device_status) */
 } bitnet_status;
 
 typedef struct CUstream_st* bitnet_stream_t; /* == cudaStream_t */
@@ -305,12 +306,123 @@ BITNET_API int bitnet_bitlinear_forward_qk(const float* x, const float* norm_w, 
                                            int64_t M, int64_t K, int64_t N, float eps, int64_t head_dim,
                                            const float* head_w, float* y, bitnet_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Projections with 8-bit weights, for the layers a model keeps at 8 bits (an
+ * output head, an embedding projection) next to its ternary ones.  Activations
+ * are the int8 codes of bitnet_rmsnorm_quant_a8; the pages have no counterpart
+ * for the weights' side, which follows the activations' (absmax, 127 steps), one
+ * scale per output channel.
+ */
+
+/* Absmax int8 quantisation of w[N, K] (fp32), row by row:
+ *   w_scale[n] = 127 / max(max_k |w[n, k]|, 1e-30),
+ *   w_codes[n, k] = clamp(rint(w[n, k] * w_scale[n]), -127, 127)
+ * each operation rounded on its own.  Rows with non-finite values get
+ * unspecified codes.  w and w_codes 16-byte, w_scale 4-byte aligned. */
+BITNET_API int bitnet_quant_w8(const float* w, int64_t N, int64_t K, int8_t* w_codes, float* w_scale,
+                               bitnet_stream_t stream);
+
+/* int8 x int8 contraction with a scale per token and per channel:
+ *   acc[m, n] = sum_k a_codes[m, k] * w_codes[n, k]                (exact integer)
+ *   y[m, n]   = ((float)acc * (1 / a_scale[m])) * (1 / w_scale[n])
+ * each reciprocal and product rounded on its own, then once to y_dtype
+ * (BITNET_DTYPE_F32, _F16 or _BF16).  All 256 code values are allowed; acc is
+ * exact for every input (it fits int32: K <= 65536).  acc_out[M, N] int32
+ * receives acc when non-NULL.  a_codes, w_codes, y, acc_out 16-byte, the scales
+ * 4-byte aligned. */
+BITNET_API int bitnet_w8a8_gemm(const int8_t* a_codes, const float* a_scale, const int8_t* w_codes,
+                                const float* w_scale, int64_t M, int64_t K, int64_t N, void* y, int y_dtype,
+                                int32_t* acc_out, bitnet_stream_t stream);
+
+/* The projection of x: RMSNorm with norm_w, per-token int8 quantisation
+ * (bitnet_rmsnorm_quant_a8 of x widened to fp32) and bitnet_w8a8_gemm of the
+ * codes, bit for bit.  x[M, K] in x_dtype, norm_w[K] fp32, y[M, N] in y_dtype. */
+BITNET_API int bitnet_w8a8_forward(const void* x, int x_dtype, const float* norm_w, const int8_t* w_codes,
+                                   const float* w_scale, int64_t M, int64_t K, int64_t N, float eps, void* y,
+                                   int y_dtype, bitnet_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A paged key/value cache held in 4 bits and attention over it: what stands
+ * between the q/k/v projections (with their head norm) and the o projection.
+ *
+ * The cache is num_pages pages of BITNET_KV4_PAGE tokens; the bytes of page p
+ * and kv head h start at (p * num_kv_heads + h) * (64 * head_dim + 1024):
+ *   [64][head_dim / 2] key codes, byte j of a token holding dimension 2j in its
+ *                      low and 2j + 1 in its high four bits,
+ *   [64][head_dim / 2] value codes, the same,
+ *   [64][2] float      (scale, minimum) of each key row,
+ *   [64][2] float      (scale, minimum) of each value row.
+ * A row of head_dim values x is stored as m = min(x), s = (max(x) - m) / 15 and
+ * code = round(15 (x - m) / (max(x) - m)), ties to even, of the exact quotient; it
+ * stands for code * s + m.  Rows whose range is below 1e-30 are stored as their
+ * minimum (s = 0, codes 0).  A row with a non-finite value stands for
+ * unspecified values; no other row is affected.
+ *
+ * Sequence b of a call owns the rows q_start[b] .. q_start[b + 1] - 1 of the
+ * call's T new tokens; they are the last of the kv_lens[b] tokens the cache
+ * holds of it, so row i of its n rows is position kv_lens[b] - n + i.  Position j
+ * lies in page page_table[b * max_pages + j / 64], slot j % 64.  Rows before
+ * q_start[0] and from q_start[num_seqs] on belong to no sequence, and rows of
+ * negative position to no token: they are neither read nor written (their
+ * attention output, for the latter, is 0).  Page-table entries of positions
+ * that a call does not reach are not looked at.
+ * The arrays are read on the device.  A length that the page table cannot hold
+ * is cut, a page outside 0 .. num_pages - 1 is skipped (its keys count as
+ * masked), and both are recorded: bitnet_last_device_status then returns
+ * BITNET_ERR_BAD_INDEX.  Two rows of one call that are stored in the same slot
+ * leave it with a mixture of both. */
+#define BITNET_KV4_PAGE 64
+
+typedef struct {
+  void* cache;               /* device, 16-byte aligned, bitnet_kv4_cache_bytes() bytes       */
+  int64_t num_pages;
+  int32_t num_kv_heads;
+  int32_t head_dim;          /* 128 or 256, else BITNET_ERR_UNSUPPORTED_SHAPE                 */
+  const int32_t* q_start;    /* device [num_seqs + 1], non-decreasing                         */
+  const int32_t* kv_lens;    /* device [num_seqs]                                             */
+  const int32_t* page_table; /* device [num_seqs, max_pages]                                  */
+  int32_t num_seqs;
+  int32_t max_pages;
+} bitnet_kv4;
+
+/* num_pages * num_kv_heads * (64 * head_dim + 1024), or 0 for an invalid shape. */
+BITNET_API size_t bitnet_kv4_cache_bytes(int64_t num_pages, int32_t num_kv_heads, int32_t head_dim);
+
+/* Quantises the key and value rows k, v [T, num_kv_heads, head_dim] (dtype
+ * BITNET_DTYPE_F32, _F16 or _BF16) into their slots of the cache.  The
+ * descriptor is a HOST struct, read before the call returns; k and v 16-byte
+ * aligned. */
+BITNET_API int bitnet_kv4_append(const bitnet_kv4* c, const void* k, const void* v, int dtype, int64_t T,
+                                 bitnet_stream_t stream);
+
+/* The inverse: k, v [T, num_kv_heads, head_dim] of the plan's rows as the values
+ * that they stand for, code * s + m in two fp32 operations, rounded once to
+ * dtype.  With q_start the running sum of kv_lens it reads whole sequences. */
+BITNET_API int bitnet_kv4_read(const bitnet_kv4* c, int64_t T, void* k, void* v, int dtype, bitnet_stream_t stream);
+
+/* out[t, h] = sum_j softmax_j(scale * q[t, h] . k_j) v_j for the query rows
+ * q, out [T, num_heads, head_dim], query head h reading kv head
+ * h / (num_heads / num_kv_heads) (num_heads a multiple of num_kv_heads).  A row
+ * at position p sees, of its sequence's kv_lens[b] tokens, those at j <= p when
+ * causal is 1, of them the last `window` (j > p - window) when window > 0, and
+ * all of them when causal is 0 (window must then be 0).  A row that sees no key
+ * gives zeros.  max_q_len: an upper bound of the sequences' row counts; rows of
+ * a longer sequence are recorded as BITNET_ERR_BAD_INDEX and may be left out.
+ * q in q_dtype, out in the same type or in BITNET_DTYPE_F32; sums, softmax and
+ * scores are fp32, products of q and of the probabilities with the cache's
+ * integer codes exact up to 2^-22 (q or probability; 16-bit q: the
+ * probabilities may be rounded to 2^-11).  scale finite. */
+BITNET_API int bitnet_kv4_attention(const bitnet_kv4* c, const void* q, int q_dtype, int64_t T, int32_t num_heads,
+                                    int32_t max_q_len, float scale, int causal, int32_t window, void* out,
+                                    int out_dtype, bitnet_stream_t stream);
+
 /* Static description of a status code (never NULL). */
 BITNET_API const char* bitnet_status_string(int status);
 
 /* Synchronises `stream`, then returns BITNET_ERR_TIMEOUT if a kernel of this
- * library on the current device gave up a bounded wait since the last call
- * (and clears that record), BITNET_ERR_CUDA if the synchronisation failed, and
+ * library on the current device gave up a bounded wait since the last call,
+ * else BITNET_ERR_BAD_INDEX if a cache call met an index out of range (and
+ * clears that record), BITNET_ERR_CUDA if the synchronisation failed, and
  * BITNET_OK otherwise. */
 BITNET_API int bitnet_last_device_status(bitnet_stream_t stream);
 

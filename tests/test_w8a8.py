@@ -1,0 +1,194 @@
+"""Projections with 8-bit weights: integers bit for bit against int64 on the CPU, outputs bit for bit against the
+header's fp32 operation order."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import bitlinear_rmsnorm_token_gb300 as bn
+
+torch = pytest.importorskip("torch")
+gpu = pytest.mark.gpu
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+FAKE, ODD = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 2)
+
+
+# ------------------------------------------------------------------ refusals (no GPU needed)
+def test_refusals():
+    L = bn.lib(build=True)
+    g, f, q = L.bitnet_w8a8_gemm, L.bitnet_w8a8_forward, L.bitnet_quant_w8
+    assert q(None, 1, 128, FAKE, FAKE, None) == bn.ERR_INVALID_ARG
+    assert q(FAKE, 0, 128, FAKE, FAKE, None) == bn.ERR_INVALID_ARG
+    assert q(FAKE, 1, 100, FAKE, FAKE, None) == bn.ERR_UNSUPPORTED_SHAPE
+    assert q(FAKE, 1, 128, ODD, FAKE, None) == bn.ERR_MISALIGNED
+    assert q(FAKE, 1, 128, FAKE, ODD, None) == bn.ERR_MISALIGNED
+    assert g(FAKE, FAKE, None, FAKE, 1, 128, 1, FAKE, 0, None, None) == bn.ERR_INVALID_ARG
+    assert g(FAKE, FAKE, FAKE, FAKE, 1, 128, 1, FAKE, 3, None, None) == bn.ERR_INVALID_ARG
+    assert g(FAKE, FAKE, FAKE, FAKE, 0, 128, 1, FAKE, 0, None, None) == bn.ERR_INVALID_ARG
+    assert g(FAKE, FAKE, FAKE, FAKE, 1, 65536 + 128, 1, FAKE, 0, None, None) == bn.ERR_UNSUPPORTED_SHAPE
+    assert g(FAKE, FAKE, FAKE, FAKE, 1 << 31, 128, 1, FAKE, 0, None, None) == bn.ERR_UNSUPPORTED_SHAPE
+    assert g(FAKE, FAKE, FAKE, FAKE, 1, 128, 1, FAKE, 0, ODD, None) == bn.ERR_MISALIGNED
+    assert g(ODD, FAKE, FAKE, FAKE, 1, 128, 1, FAKE, 0, None, None) == bn.ERR_MISALIGNED
+    assert f(FAKE, 0, FAKE, FAKE, FAKE, 1, 128, 1, 0.0, FAKE, 0, None) == bn.ERR_INVALID_ARG
+    assert f(FAKE, 7, FAKE, FAKE, FAKE, 1, 128, 1, 1e-6, FAKE, 0, None) == bn.ERR_INVALID_ARG
+    assert f(FAKE, 0, FAKE, FAKE, FAKE, 1, 64, 1, 1e-6, FAKE, 0, None) == bn.ERR_UNSUPPORTED_SHAPE
+    assert f(FAKE, 0, ODD, FAKE, FAKE, 1, 128, 1, 1e-6, FAKE, 0, None) == bn.ERR_MISALIGNED
+
+
+def test_binding_refusals():
+    z = torch.zeros
+    c, w = z((2, 128), dtype=torch.int8), z((4, 128), dtype=torch.int8)
+    with pytest.raises(ValueError):  # not on a GPU
+        bn.w8a8_gemm(c, z(2), w, z(4))
+    with pytest.raises(ValueError):  # another K
+        bn.w8a8_gemm(c, z(2), z((4, 256), dtype=torch.int8), z(4))
+    with pytest.raises(ValueError):  # one scale too few
+        bn.w8a8_gemm(c, z(2), w, z(3))
+    with pytest.raises(TypeError):
+        bn.w8a8_gemm(c, z(2), w, z(4), y_dtype=torch.float64)
+    with pytest.raises(ValueError):
+        bn.w8a8_forward(z((2, 128)), z(64), w, z(4))
+
+
+# ------------------------------------------------------------------ GPU
+@pytest.fixture(scope="module")
+def device():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    bn.lib(build=True)
+    yield
+    assert bn.last_device_status() == bn.OK
+
+
+def exact_y(acc, a_scale, w_scale, dtype):
+    one = np.float32(1)
+    y = (acc.astype(np.float32) * (one / a_scale)[:, None]) * (one / w_scale)[None, :]
+    return torch.from_numpy(y.astype(np.float32)).to(dtype)
+
+
+def codes(seed, shape, kind="any"):
+    r = np.random.default_rng(seed)
+    if kind == "any":
+        return r.integers(-128, 128, shape).astype(np.int8)
+    if kind == "low":
+        return np.full(shape, -128, np.int8)
+    return np.where(r.random(shape) < 0.5, np.int8(127), np.int8(-128)).astype(np.int8)
+
+
+def check_gemm(M, K, N, dtype=F32, ka="any", kw="any", acc=True):
+    a, w = codes(M + K, (M, K), ka), codes(N + K, (N, K), kw)
+    r = np.random.default_rng(7)
+    sa, sw = r.uniform(5, 60, M).astype(np.float32), r.uniform(500, 5000, N).astype(np.float32)
+    # float64 products of int8 codes and their sums (below 2^53) are exact
+    want = (a.astype(np.float64) @ w.astype(np.float64).T).astype(np.int64)
+    t = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+    pad = torch.full((M * N + 256,), 3.0, dtype=dtype, device="cuda")
+    out = pad[128:128 + M * N].view(M, N)
+    acc_out = torch.full((M, N), -7, dtype=torch.int32, device="cuda") if acc else None
+    bn.w8a8_gemm(t(a), t(sa), t(w), t(sw), y=out, acc_out=acc_out)
+    if acc:
+        assert np.array_equal(acc_out.cpu().numpy(), want)
+    assert torch.equal(out.cpu(), exact_y(want, sa, sw, dtype))
+    assert torch.all(pad[:128] == 3.0) and torch.all(pad[128 + M * N:] == 3.0)
+
+
+@gpu
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 7, 8, 9, 13, 16, 17, 31, 33, 63, 64, 65, 100, 129, 200, 300])
+@pytest.mark.parametrize("K,N", [(128, 1), (256, 130), (640, 256), (1152, 77)])
+def test_gemm_small(device, M, K, N):
+    check_gemm(M, K, N, acc=True)
+    check_gemm(M, K, N, acc=False)
+
+
+@gpu
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 1000), (3, 16384, 520), (8, 8192, 257), (13, 8192, 1024), (50, 4096, 2056),
+                                   (64, 2048, 640), (257, 4096, 1032), (1000, 1024, 2048), (700, 2176, 1336),
+                                   (16, 65536, 130), (2, 65536, 9), (130, 65536, 136)])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_gemm_large(device, M, K, N, dtype):
+    check_gemm(M, K, N, dtype, acc=False)
+
+
+@gpu
+@pytest.mark.parametrize("M", [1, 6, 20, 64, 150])
+@pytest.mark.parametrize("ka,kw", [("low", "low"), ("ends", "ends"), ("low", "ends")])
+def test_gemm_extreme_codes(device, M, ka, kw):
+    """Every code at the end of its range: sums up to 2^14 K, beyond 2^24 from K = 1024 on."""
+    for K in (1024, 1152, 8192, 65536):
+        check_gemm(M, K, 140, F32, ka, kw)
+
+
+@gpu
+@pytest.mark.parametrize("N,K", [(1, 128), (9, 640), (130, 4096)])
+def test_quant_w8(device, N, K):
+    r = np.random.default_rng(3)
+    w = (r.standard_normal((N, K)) * 10.0 ** r.integers(-6, 6, (N, 1))).astype(np.float32)
+    if N > 3:
+        w[1] = 0.0
+        w[2] = 1e-38
+        w[3, :2] = [0.5, -127.0]
+        w[3, 2:] = np.where(r.random(K - 2) < 0.5, 0.5, 1.5)  # ties: rint(0.5) = 0, rint(1.5) = 2
+    codes_d, scale_d = bn.quant_w8(torch.from_numpy(w).cuda())
+    sc = (np.float32(127) / np.maximum(np.abs(w).max(1), np.float32(1e-30))).astype(np.float32)
+    want = np.clip(np.rint((w * sc[:, None]).astype(np.float32)), -127, 127).astype(np.int8)
+    assert np.array_equal(scale_d.cpu().numpy(), sc)
+    assert np.array_equal(codes_d.cpu().numpy(), want)
+
+
+@gpu
+@pytest.mark.parametrize("M", [1, 5, 8, 9, 40, 100])
+@pytest.mark.parametrize("K,N", [(640, 96), (4096, 264)])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_forward_is_its_steps(device, M, K, N, dtype):
+    """norm + quantisation + product, bit for bit the entry points one by one."""
+    r = np.random.default_rng(5)
+    x = torch.from_numpy(r.standard_normal((M, K)).astype(np.float32) * 3).to(dtype).cuda()
+    g = torch.from_numpy((1 + 0.1 * r.standard_normal(K)).astype(np.float32)).cuda()
+    w, sw = bn.quant_w8(torch.from_numpy((0.02 * r.standard_normal((N, K))).astype(np.float32)).cuda())
+    a, sa, _ = bn.rmsnorm_quant_a8(x.float(), g)
+    for yt in {dtype, F32}:
+        want = bn.w8a8_gemm(a, sa, w, sw, y_dtype=yt)
+        got = bn.w8a8_forward(x, g, w, sw, y_dtype=yt)
+        assert torch.equal(got, want)
+    # against 64 bits: the two quantisations and one rounding stand between.  A quantisation's error is uniform in half a
+    # step, max / 127, on values whose max is below 6 times their rms: 6 / (127 sqrt(12)) = 1.4 %, the two 2 %, and a row
+    # of at least 96 outputs scatters by less than half of that
+    xf = x.double()
+    xn = xf * torch.rsqrt(xf.square().mean(1, keepdim=True) + 1e-6) * g.double()
+    y64 = xn @ (w.double() / sw.double()[:, None]).T
+    rel = ((got.double() - y64).norm(dim=1) / y64.norm(dim=1)).max()
+    assert rel < 0.03 + torch.finfo(dtype).eps
+
+
+@gpu
+@pytest.mark.parametrize("M", [1, 20, 200])
+def test_streams_and_graphs(device, M):
+    K, N = 2048, 520
+    t = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+    w, sw = t(codes(1, (N, K))), torch.rand(N, device="cuda") + 1
+    a = [t(codes(2 + i, (M, K))) for i in range(2)]
+    sa = torch.rand(M, device="cuda") + 1
+    want = [bn.w8a8_gemm(x, sa, w, sw) for x in a]
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [torch.zeros_like(want[0]) for _ in a]
+    for i in range(2):  # at once on two streams
+        with torch.cuda.stream(s[i]):
+            bn.w8a8_gemm(a[i], sa, w, sw, y=outs[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, v) for o, v in zip(outs, want))
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            bn.w8a8_gemm(a[i], sa, w, sw, y=outs[i])
+        graphs.append(g)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(s[i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, v) for o, v in zip(outs, want))
