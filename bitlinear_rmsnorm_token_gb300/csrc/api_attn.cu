@@ -139,8 +139,10 @@ int bitnet_kv4_attention(const bitnet_kv4* c, const void* q, int q_dtype, int64_
   if (!aligned16(q) || !aligned16(out)) return BITNET_ERR_MISALIGNED;
   DeviceContext* ctx;
   if ((rc = device_context(&ctx))) return rc;
-  return cuda_status(launch_kv4_attention(ctx, view, c->head_dim, q, q_dtype, T, num_heads, max_q_len, scale, causal,
-                                          window, out, out_dtype, reinterpret_cast<cudaStream_t>(stream)));
+  int st = BITNET_OK;
+  const cudaError_t e = launch_kv4_attention(ctx, view, c->head_dim, q, q_dtype, T, num_heads, max_q_len, scale, causal,
+                                             window, out, out_dtype, reinterpret_cast<cudaStream_t>(stream), &st);
+  return st != BITNET_OK ? st : cuda_status(e);
 }
 
 }  // extern "C"

@@ -115,7 +115,12 @@ cudaError_t launch_d(const DeviceContext* ctx, const KvView& c, int head_dim, co
 
 cudaError_t launch_kv4_attention(DeviceContext* ctx, const KvView& c, int head_dim, const void* q, int q_dtype,
                                  int64_t T, int Hq, int max_q_len, float scale, int causal, int window, void* out,
-                                 int out_dtype, cudaStream_t s) {
+                                 int out_dtype, cudaStream_t s, int* status) {
+  *status = BITNET_OK;
+  const int64_t rows = static_cast<int64_t>(Hq / c.heads) * max_q_len;
+  if (kv4_decode_supported(head_dim, q_dtype, rows))
+    return launch_kv4_decode(ctx, c, head_dim, q, q_dtype, T, Hq, rows, scale, causal, window, out, out_dtype, s,
+                             status);
   auto with_out = [&](auto* qt) {
     using QT = std::remove_pointer_t<decltype(qt)>;
     if (out_dtype == BITNET_DTYPE_F32)

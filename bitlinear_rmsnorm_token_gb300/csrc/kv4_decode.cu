@@ -1,0 +1,778 @@
+// kv4_decode.cu -- attention of a few query rows per sequence over the paged
+// 4-bit cache (single-token decode, speculation): one pass over the cache, split
+// evenly over the GPU whatever the sequences' lengths.
+//
+// Work: an item is a (sequence, kv head) with its G * n query rows; a unit is
+// one page (64 tokens) of an item.  The units of all items, in order, are dealt
+// out in equal contiguous ranges to the consumer warps of a persistent grid, so
+// a batch of ragged lengths keeps every warp equally busy.  The piece of an item
+// inside a warp's range is a segment: a segment that is the whole item writes
+// the output, the others their partial sums, joined in order by a second launch
+// (no atomics: the same bits every time).
+//
+// A warp owns its ring of page slots; lane w of the producer warp walks warp
+// w's units, brings each page block (codes, scales and minima of 64 tokens, one
+// contiguous bulk copy) and a small descriptor into the ring, so the consumers
+// touch global memory only for queries and results.
+//
+// Products run on mma.m16n8k16 (fp16 x fp16, fp32 sums) with the cache as the
+// 16-row side and the query rows as the 8-column side: a page is read once for
+// all rows of its item, and the work stays far below what feeding it costs
+// (tcgen05 would take a 128-row tile for these 8 columns).
+//   S^T[64 keys, cols] = C_k q^T:  the 4-bit codes themselves are the operand.
+//     A code masked out of its word is the fp16 subnormal c 2^-24 (or 16 c 2^-24
+//     from the higher nibble, met by q / 16): one AND per two codes.
+//     q . k_j = s_j (q . c_j) + m_j sum(q).
+//   O^T[D, cols] = C_v^T W:  W = p_j s_j as fp16, the same encoding of c_j, pairs
+//     of keys put side by side by a byte permute.  sum p_j m_j is a scalar per
+//     row.  W is kept in fp16's range by a power of two of the largest s_j met.
+// Queries are scaled by a power of two per row.  fp32 queries are two fp16
+// parts in neighbouring columns (hi, lo: 22 bits), as is W then; a 16-bit query
+// is one fp16 exactly, and W takes two parts whenever the columns suffice.
+// With one part (2^-11), the error that rounding W makes at the middle of a
+// row's range (code 7.5) is added back as part of the scalar, which leaves what
+// rounding probabilities against centred values would.
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+#include "rowquant.cuh"
+
+namespace bitnet {
+namespace {
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// D += A B, one m16n8k16 fp16 product (rows x k: A, k x columns: B).
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8x8 matrix of 16-bit values held as mma fragments.
+__device__ __forceinline__ uint32_t movm(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(__half a, __half b) {
+  return static_cast<uint32_t>(__half_as_ushort(a)) | (static_cast<uint32_t>(__half_as_ushort(b)) << 16);
+}
+
+// 2^(14 - e) for 2^e <= v < 2^(e+1), e kept in [-100, 110]: v times it is below 2^15.
+__device__ __forceinline__ int pow2_exp(float v) {
+  const int e = (__float_as_int(v) >> 23) - 127;
+  return min(max(e, -100), 110);
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
+
+// What a consumer needs to know of a page.
+struct __align__(16) Unit {
+  int key0;    // position of the page's first token
+  int len;     // tokens of the sequence
+  int n;       // its query rows (tokens)
+  int q0;      // first of them in q
+  int head;    // kv head
+  int flags;   // kValid ...
+  int item;    // sequence * heads + head
+  int pad;
+};
+constexpr int kValid = 1, kFirst = 2, kLast = 4, kWhole = 8;
+
+template <int D, int kWarps_, int kStages_>
+struct Layout {
+  static constexpr int kWarps = kWarps_;  // consumer warps; one more produces
+  static constexpr int kStages = kStages_;
+  static constexpr int kThreads = (kWarps + 1) * 32;
+  static constexpr int kSlots = kWarps * kStages;
+  static constexpr int offUnit = kSlots * KvBlock<D>::kBytes;
+  static constexpr int offBar = offUnit + kSlots * static_cast<int>(sizeof(Unit));
+  static constexpr int offScan = offBar + 2 * kSlots * 8;
+  static constexpr int offMisc = offScan + kThreads * 4;  // per-warp sums, abort flag
+  static constexpr int kBytes = offMisc + 128;
+  static_assert(kBytes <= 232448, "over the 227 KB of shared memory a CTA may use");
+};
+
+struct Problem {
+  KvView c;
+  int Hq, G, T;
+  int max_rows;   // rows of an item this launch can hold
+  float scale;    // softmax scale * log2(e)
+  int causal, window;
+  unsigned* err;
+  float* part;    // [items + warps][rows][D + 2]: o, m, l of the segments
+  int2* ends;     // [items]: first and last warp of the item
+  int rows;       // rows per partial
+};
+
+// First key and count of the pages that sequence b's rows look at; 0 pages for
+// a sequence without rows or with a malformed plan (recorded).
+__device__ __forceinline__ int seq_pages(const Problem& p, int b, int* first, int* len, int* n, int* q0) {
+  bool bad = false;
+  *q0 = p.c.q_start[b];
+  *n = p.c.q_start[b + 1] - *q0;
+  *len = kv_len_of(p.c, b, &bad);
+  if (*n < 0 || *q0 < 0 || *q0 + static_cast<int64_t>(*n) > p.T || static_cast<int64_t>(*n) * p.G > p.max_rows) {
+    bad = true;
+    *n = 0;
+  }
+  if (bad) atomicOr(p.err, kErrBadIndex);
+  if (*n <= 0) return 0;
+  int64_t lo = 0;
+  if (p.causal && p.window > 0) lo = max(static_cast<int64_t>(0), static_cast<int64_t>(*len) - *n - p.window + 1);
+  *first = static_cast<int>(lo / kKvPage);
+  return max(1, (*len + kKvPage - 1) / kKvPage - *first);
+}
+
+template <int D, int NB, bool kSplit, typename QT, typename OT, class L>
+__global__ void __launch_bounds__(L::kThreads, 1)
+    k_kv4_decode(const Problem p, const QT* __restrict__ q, OT* __restrict__ out) {
+  using B = KvBlock<D>;
+  constexpr int kWarps = L::kWarps, kStages = L::kStages;
+  constexpr int kRowsNb = kSplit ? 4 : 8;    // query rows per 8 columns
+  constexpr int kWordsK = D / 32;            // words of a key row per lane (a quarter row)
+  constexpr int kTiles = D / 16;             // 16-dimension tiles of the output
+  constexpr int kCols = kSplit ? 1 : 2;      // scores per key, column block and lane
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Unit* units = reinterpret_cast<Unit*>(smem + L::offUnit);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::offBar);
+  uint64_t* empty = full + L::kSlots;
+  int* scan = reinterpret_cast<int*>(smem + L::offScan);
+  int* misc = reinterpret_cast<int*>(smem + L::offMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 16);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int B_seqs = p.c.num_seqs, H = p.c.heads;
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  // ---- total pages, then the sequence where each warp's range begins
+  auto pages_of = [&](int b) {
+    int f, l, n, q0;
+    return b < B_seqs ? seq_pages(p, b, &f, &l, &n, &q0) : 0;
+  };
+  int mine = 0;
+  for (int b = threadIdx.x; b < B_seqs; b += L::kThreads) mine += pages_of(b);
+  int s = warp_sum_int(mine);
+  if (lane == 0) misc[warp] = s;
+  __syncthreads();
+  int64_t total = 0;
+  for (int w = 0; w <= kWarps; ++w) total += misc[w];
+  const int64_t U = total * H;
+  // warp i of CTA c is number i * grid + c, so that few units spread over the CTAs; with fewer units than warps the
+  // first U warps take one each
+  const int64_t W = min(static_cast<int64_t>(gridDim.x) * kWarps, U);
+  const int my_warp = warp < kWarps ? warp : lane;  // the producer's lanes: the warp that they serve
+  const int64_t w_me = static_cast<int64_t>(my_warp) * gridDim.x + blockIdx.x;
+  const bool has = my_warp < kWarps && w_me < W;
+  const int64_t u0 = has ? U * w_me / W : 0, u1 = has ? U * (w_me + 1) / W : 0;
+
+  if (warp < kWarps) {
+    // the scan below is the producer's; the consumers only take part in it
+    for (int c0 = 0; c0 < B_seqs; c0 += L::kThreads) {
+      const int v = pages_of(c0 + threadIdx.x);
+      int x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      scan[threadIdx.x] = x;
+      if (lane == 31) misc[warp] = x;
+      __syncthreads();
+    }
+    __syncthreads();
+    // ------------------------------------------------------------ consumer
+    const int g = lane >> 2, t = lane & 3;
+    const int pg = g ^ ((g >> 1) & 1);  // key of tile row g: spreads the rows that lanes read together over the banks
+    float acc[NB][kTiles][4];
+    float m_run[NB][kCols], l_run[NB][kCols], z_run[NB][kCols], qsum[NB][kCols], qc[NB][kCols];
+    uint32_t qf[NB][kWordsK][4];
+    int e_run = -100;
+    const int64_t count = u1 - u0;
+    for (int64_t k = 0; k < count; ++k) {
+      const int slot = warp * kStages + static_cast<int>(k % kStages);
+      if (!mbar_wait(&full[slot], static_cast<unsigned>((k / kStages) & 1), p.err, abort_flag)) break;
+      const Unit un = units[slot];
+      const uint8_t* blk = smem + slot * B::kBytes;
+      const int rows = un.n * p.G;
+      if (un.flags & kFirst) {
+        // ---- the item's queries as B fragments: column g, dimensions (D / 4) t ..
+        e_run = -100;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[nb][i][j] = 0.0f;
+          const int r = nb * kRowsNb + (kSplit ? g >> 1 : g);
+          const bool on = r < rows;
+          const int i_tok = on ? r / p.G : 0;
+          const QT* src = q + (static_cast<int64_t>(un.q0 + i_tok) * p.Hq + un.head * p.G + (on ? r - i_tok * p.G : 0)) * D +
+                          (D / 4) * t;
+          float v[D / 4], top = 0.0f;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const float4 x = on ? load4(src + 4 * i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            v[4 * i] = x.x;
+            v[4 * i + 1] = x.y;
+            v[4 * i + 2] = x.z;
+            v[4 * i + 3] = x.w;
+          }
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(v[i]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = pow2_exp(top);
+          const float f = pow2(14 - e);
+          float sum = 0.0f;
+          __half h[D / 4];
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) {
+            const float x = v[i] * f;
+            h[i] = __float2half_rn(x);
+            if (kSplit && (g & 1)) h[i] = __float2half_rn(x - __half2float(h[i]));
+            sum += __half2float(h[i]);
+          }
+#pragma unroll
+          for (int w = 0; w < kWordsK; ++w) {
+            const __half inv16 = __float2half_rn(0.0625f);
+            const __half* x = h + 8 * w;
+            qf[nb][w][0] = pack_h2(x[0], x[4]);
+            qf[nb][w][1] = pack_h2(__hmul(x[1], inv16), __hmul(x[5], inv16));
+            qf[nb][w][2] = pack_h2(x[2], x[6]);
+            qf[nb][w][3] = pack_h2(__hmul(x[3], inv16), __hmul(x[7], inv16));
+          }
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          // to the lanes that hold the scores of these columns: 2t and 2t + 1
+          const float s0 = __shfl_sync(0xffffffffu, sum, 8 * t), s1 = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+          const int e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
+          // S comes in units of 2^-24: sum(q) likewise, undone with the row's power of two in qc
+          qsum[nb][0] = (kSplit ? s0 + s1 : s0) * 0x1p-24f;
+          qc[nb][0] = p.scale * pow2(e0 - 14) * 0x1p24f;
+          if constexpr (!kSplit) {
+            qsum[nb][1] = s1 * 0x1p-24f;
+            qc[nb][1] = p.scale * pow2(e1 - 14) * 0x1p24f;
+          }
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            m_run[nb][j] = -INFINITY;
+            l_run[nb][j] = 0.0f;
+            z_run[nb][j] = 0.0f;
+          }
+        }
+      }
+      if (un.flags & kValid) {
+        // ---- scores of the page's 64 keys: tile kt, rows g and g + 8
+        float sc[NB][4][4];
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sc[nb][kt][j] = 0.0f;
+          const uint4* r0 = reinterpret_cast<const uint4*>(blk + B::offK + (16 * kt + pg) * B::kRow + (B::kRow / 4) * t);
+          const uint4* r1 = reinterpret_cast<const uint4*>(blk + B::offK + (16 * kt + pg + 8) * B::kRow + (B::kRow / 4) * t);
+#pragma unroll
+          for (int c = 0; c < kWordsK / 4; ++c) {
+            const uint4 a = r0[c], b = r1[c];
+            const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t ah = wa[i] >> 8, bh = wb[i] >> 8;
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                const uint32_t* f = qf[nb][4 * c + i];
+                mma16816(sc[nb][kt], wa[i] & 0x000f000fu, wb[i] & 0x000f000fu, wa[i] & 0x00f000f0u, wb[i] & 0x00f000f0u,
+                         f[0], f[1]);
+                mma16816(sc[nb][kt], ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u, bh & 0x00f000f0u, f[2], f[3]);
+              }
+            }
+          }
+        }
+        // ---- scores to exponents of two, masks, the rows' maxima
+        const int pos0 = un.len - un.n;  // position of the item's first query token
+        const bool inner = un.key0 + kKvPage <= (p.causal ? pos0 + 1 : un.len) &&
+                           (!p.causal || p.window == 0 || un.key0 > un.len - 1 - p.window);
+        float x[NB][8][kCols], mx[NB][kCols];
+        float vs[8], vm[8], smax = 0.0f;
+        const float2* kmeta = reinterpret_cast<const float2*>(blk + B::offKMeta);
+        const float2* vmeta = reinterpret_cast<const float2*>(blk + B::offVMeta);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) mx[nb][j] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int key = 16 * (i >> 1) + 8 * (i & 1) + pg;
+          const float2 km = kmeta[key], vv = vmeta[key];
+          vs[i] = vv.x;
+          vm[i] = vv.y;
+          if (!inner && un.key0 + key >= un.len) vs[i] = vm[i] = 0.0f;  // a slot without a token: any bytes
+          smax = fmaxf(smax, vs[i]);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) {
+              const float* s4 = sc[nb][i >> 1] + 2 * (i & 1);
+              const float dot = kSplit ? s4[0] + s4[1] : s4[j];
+              x[nb][i][j] = fmaf(dot, km.x, km.y * qsum[nb][j]) * qc[nb][j];
+            }
+          }
+        }
+        if (!inner) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) {
+              const int r = nb * kRowsNb + (kSplit ? t : 2 * t + j);
+              const int pos = r < rows ? pos0 + r / p.G : un.len - 1;
+              const int hi = p.causal ? min(pos, un.len - 1) : un.len - 1;
+              const int lo = p.causal && p.window > 0 ? pos - p.window + 1 : 0;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int key = un.key0 + 16 * (i >> 1) + 8 * (i & 1) + pg;
+                if (key > hi || key < lo) x[nb][i][j] = -INFINITY;
+              }
+            }
+        }
+        smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 4));
+        smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 8));
+        smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 16));
+        const int e_new = max(e_run, pow2_exp(smax));
+        bool moved = e_new != e_run;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            float v = x[nb][0][j];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) v = fmaxf(v, x[nb][i][j]);
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            mx[nb][j] = fmaxf(m_run[nb][j], v);
+            moved |= mx[nb][j] != m_run[nb][j];
+          }
+        if (__any_sync(0xffffffffu, moved)) {
+          const float fe = e_new == e_run ? 1.0f : ex2(static_cast<float>(e_run - e_new));
+          e_run = e_new;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            float a[2];
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) {
+              // nothing seen so far: every sum is 0, and -inf - -inf must not reach the exponential
+              const float al = m_run[nb][j] == -INFINITY ? 0.0f : ex2(m_run[nb][j] - mx[nb][j]);
+              m_run[nb][j] = mx[nb][j];
+              l_run[nb][j] *= al;
+              z_run[nb][j] *= al;
+              a[j] = al * fe;
+            }
+            if constexpr (kSplit) a[1] = a[0];
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+              acc[nb][i][0] *= a[0];
+              acc[nb][i][1] *= a[1];
+              acc[nb][i][2] *= a[0];
+              acc[nb][i][3] *= a[1];
+            }
+          }
+        }
+        // ---- probabilities, their sums, and W as B fragments
+        const float vf = pow2(14 - e_run);
+        [[maybe_unused]] const float mid = 7.5f * pow2(e_run - 14);
+        uint32_t wf[NB][4][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float mref[kCols];
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) mref[j] = m_run[nb][j] == -INFINITY ? 0.0f : m_run[nb][j];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            __half hw[2];
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) {
+              const bool none = !inner && x[nb][i][j] == -INFINITY;  // masked: whatever its value row holds
+              const float pr = ex2(x[nb][i][j] - mref[j]);
+              const float w = none ? 0.0f : pr * (vs[i] * vf);
+              l_run[nb][j] += pr;
+              const __half h = __float2half_rn(w);
+              const float rest = w - __half2float(h);
+              float zi = none ? 0.0f : pr * vm[i];
+              if constexpr (kSplit) {
+                hw[0] = h;
+                hw[1] = __float2half_rn(rest);
+              } else {
+                hw[j] = h;
+                zi = fmaf(rest, mid, zi);
+              }
+              z_run[nb][j] += zi;
+            }
+            wf[nb][i >> 1][i & 1] = movm(pack_h2(hw[0], hw[1]));
+          }
+        }
+        // ---- O^T += C_v^T W: keys 2t, 2t + 1 (and 8 on) of tile kt, this lane's 2 kTiles dimensions of each
+        const int k0 = (2 * t) ^ (t & 1), k1 = (2 * t + 1) ^ (t & 1);  // keys of tile rows 2t, 2t + 1
+        constexpr int kVw = D / 64;  // words of a value row per lane
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+          uint32_t w[4][kVw];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int key = 16 * kt + 8 * (r >> 1) + ((r & 1) ? k1 : k0);
+            const uint8_t* src = blk + B::offV + key * B::kRow + 4 * kVw * g;
+            if constexpr (kVw == 2) {
+              const uint2 v = *reinterpret_cast<const uint2*>(src);
+              w[r][0] = v.x;
+              w[r][1] = v.y;
+            } else {
+              const uint4 v = *reinterpret_cast<const uint4*>(src);
+              w[r][0] = v.x;
+              w[r][1] = v.y;
+              w[r][2] = v.z;
+              w[r][3] = v.w;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) {
+            // byte i of both keys in the two halves: low nibbles dimension 2i, high nibbles 2i + 1
+            const uint32_t sel = (i & 3) | ((4 + (i & 3)) << 8);
+            const uint32_t a = prmt_b32(w[0][i >> 2], w[1][i >> 2], sel);
+            const uint32_t b = prmt_b32(w[2][i >> 2], w[3][i >> 2], sel);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma16816(acc[nb][i], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, wf[nb][kt][0],
+                       wf[nb][kt][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
+      if (un.flags & kLast) {
+        // ---- the segment's sums: whole items to the output, others to their partial
+        const float un_w = 0x1p24f * pow2(e_run - 14);  // undoes the codes' 2^-24 and W's power of two
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            float l = l_run[nb][j], z = z_run[nb][j];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              l += __shfl_xor_sync(0xffffffffu, l, o);
+              z += __shfl_xor_sync(0xffffffffu, z, o);
+            }
+            const int r = nb * kRowsNb + (kSplit ? t : 2 * t + j);
+            if (r >= rows) continue;
+            float o[2 * kTiles];
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+              const float lo = kSplit ? acc[nb][i][0] + acc[nb][i][1] : acc[nb][i][j];
+              const float hi = kSplit ? acc[nb][i][2] + acc[nb][i][3] : acc[nb][i][2 + j];
+              o[2 * i] = fmaf(lo, un_w, z);
+              o[2 * i + 1] = fmaf(hi, un_w * 0.0625f, z);
+            }
+            if (un.flags & kWhole) {
+              const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // no key seen: zeros; NaN stays
+              const int i_tok = r / p.G;
+              OT* dst = out + (static_cast<int64_t>(un.q0 + i_tok) * p.Hq + un.head * p.G + (r - i_tok * p.G)) * D +
+                        2 * kTiles * g;
+              constexpr int kPer = 16 / static_cast<int>(sizeof(OT));
+#pragma unroll
+              for (int i = 0; i < 2 * kTiles / kPer; ++i) {
+                union { OT v[kPer]; uint4 u; } pk;
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) pk.v[c] = round_out<OT>(o[i * kPer + c] * inv);
+                reinterpret_cast<uint4*>(dst)[i] = pk.u;
+              }
+            } else {
+              float* dst = p.part + ((un.item + w_me) * p.rows + r) * (D + 4);
+#pragma unroll
+              for (int i = 0; i < kTiles / 2; ++i)
+                reinterpret_cast<float4*>(dst + 2 * kTiles * g)[i] =
+                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              if (g == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(m_run[nb][j], l);
+            }
+          }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ producer
+    int b = 0;
+    int64_t base = 0, before = 0;  // pages before the chunk, and before sequence b
+    for (int c0 = 0; c0 < B_seqs; c0 += L::kThreads) {
+      const int v = pages_of(c0 + threadIdx.x);
+      int x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      scan[threadIdx.x] = x;
+      if (lane == 31) misc[warp] = x;
+      __syncthreads();
+      const int64_t want = u0 / H - base;  // page of the chunk where the range begins
+      int64_t chunk = 0;
+      for (int w = 0; w <= kWarps; ++w) {
+        const int64_t in = misc[w];
+        if (u0 < u1 && want >= chunk && want < chunk + in) {
+          int i = 0;  // first of the warp's 32 sequences whose running sum passes it
+          while (scan[32 * w + i] <= want - chunk) ++i;
+          b = c0 + 32 * w + i;
+          before = base + chunk + (i ? scan[32 * w + i - 1] : 0);
+        }
+        chunk += in;
+      }
+      base += chunk;
+    }
+    __syncthreads();
+    if (lane < kWarps) {
+      int first = 0, len = 0, n = 0, q0 = 0, pages = 0, h = 0, pg = 0;
+      if (u0 < u1) {
+        pages = seq_pages(p, b, &first, &len, &n, &q0);
+        const int64_t o = u0 - before * H;
+        h = static_cast<int>(o / pages);
+        pg = static_cast<int>(o - static_cast<int64_t>(h) * pages);
+      }
+      const int64_t count = u1 - u0;
+      bool fresh = true;  // the segment's first page
+      int64_t seg0 = 0;   // and its place in the range
+      int64_t k = 0;
+      // The lanes poll without blocking, each going on as soon as its own warp has freed a slot.
+      unsigned long long since = global_timer_ns();
+      while (k < count) {
+        const int slot = lane * kStages + static_cast<int>(k % kStages);
+        if (!mbar_test(&empty[slot], static_cast<unsigned>((k / kStages) & 1) ^ 1u)) {
+          if (*abort_flag) break;
+          if (global_timer_ns() - since > kWaitTimeoutNs) {
+            atomicOr(p.err, kErrWaitTimeout);
+            *abort_flag = 1;
+            break;
+          }
+          __nanosleep(40);
+          continue;
+        }
+        const int page_i = first + pg;
+        int page = -1;
+        if (len > 0) {
+          page = p.c.page_table[static_cast<int64_t>(b) * p.c.max_pages + page_i];
+          if (page < 0 || page >= p.c.num_pages) {
+            page = -1;
+            atomicOr(p.err, kErrBadIndex);
+          }
+        }
+        if (fresh) {
+          seg0 = k;
+          if (pg == 0) {  // this range holds the item's beginning: say where it ends
+            const int64_t z = u0 + k + pages - 1;
+            p.ends[static_cast<int64_t>(b) * H + h] =
+                make_int2(static_cast<int>(w_me), static_cast<int>(((z + 1) * W - 1) / U));
+          }
+        }
+        const bool last_of_item = pg == pages - 1;
+        Unit un;
+        un.key0 = page_i * kKvPage;
+        un.len = len;
+        un.n = n;
+        un.q0 = q0;
+        un.head = h;
+        un.item = b * H + h;
+        un.flags = (page >= 0 ? kValid : 0) | (fresh ? kFirst : 0) | (last_of_item || k == count - 1 ? kLast : 0) |
+                   (last_of_item && k - seg0 == pages - 1 ? kWhole : 0);
+        un.pad = 0;
+        units[slot] = un;
+        if (page >= 0) {
+          mbar_arrive_expect_tx(&full[slot], B::kBytes);
+          bulk_load(smem + slot * B::kBytes, p.c.cache + (static_cast<int64_t>(page) * H + h) * B::kBytes, B::kBytes,
+                    &full[slot]);
+        } else {
+          mbar_arrive(&full[slot]);
+        }
+        since = global_timer_ns();
+        fresh = last_of_item;
+        if (++pg == pages && k + 1 < count) {
+          pg = 0;
+          if (++h == H) {
+            h = 0;
+            do {
+              ++b;
+              pages = b < B_seqs ? seq_pages(p, b, &first, &len, &n, &q0) : 1;
+            } while (pages == 0);
+          }
+        }
+        ++k;
+      }
+      if (*abort_flag)  // given up: copies still in flight must land before the CTA's shared memory goes
+        for (int64_t i = max(static_cast<int64_t>(0), k - kStages); i < k; ++i)
+          mbar_wait(&full[lane * kStages + static_cast<int>(i % kStages)], static_cast<unsigned>((i / kStages) & 1), p.err);
+    }
+  }
+}
+
+// Joins the segments of the items that several warps shared: one CTA per item,
+// a thread per output element, segments in order.
+template <int D, typename OT>
+__global__ void __launch_bounds__(256) k_kv4_join(const Problem p, OT* __restrict__ out) {
+  __shared__ float s_f[64];
+  pdl_wait();
+  const int item = blockIdx.x, b = item / p.c.heads, h = item - b * p.c.heads;
+  const int q0 = p.c.q_start[b], n = p.c.q_start[b + 1] - q0;
+  if (n <= 0 || q0 < 0 || static_cast<int64_t>(q0) + n > p.T || static_cast<int64_t>(n) * p.G > p.max_rows) return;
+  const int2 e = p.ends[item];
+  if (e.x == e.y) return;
+  const int segs = e.y - e.x + 1;
+  const float* part = p.part + (static_cast<int64_t>(item) + e.x) * p.rows * (D + 4);
+  const int64_t stride = static_cast<int64_t>(p.rows) * (D + 4);
+  const int rows = n * p.G;
+  for (int r = 0; r < rows; ++r) {
+    const float* pr = part + static_cast<int64_t>(r) * (D + 4);
+    float m = -INFINITY;
+    for (int i = threadIdx.x & 31; i < segs; i += 32) m = fmaxf(m, pr[i * stride + D]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == -INFINITY) m = 0.0f;
+    float o = 0.0f, l = 0.0f;
+    for (int i0 = 0; i0 < segs; i0 += 64) {
+      __syncthreads();
+      const int i = i0 + threadIdx.x;
+      if (threadIdx.x < 64) s_f[threadIdx.x] = i < segs ? ex2(pr[i * stride + D] - m) : 0.0f;
+      __syncthreads();
+      const int most = min(64, segs - i0);
+      if (threadIdx.x < D) {
+        const float* src = pr + i0 * stride;
+#pragma unroll 8
+        for (int j = 0; j < most; ++j) {
+          o = fmaf(s_f[j], src[j * stride + threadIdx.x], o);
+          l = fmaf(s_f[j], src[j * stride + D + 1], l);
+        }
+      }
+    }
+    if (threadIdx.x < D) {
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+      const int i_tok = r / p.G;
+      out[(static_cast<int64_t>(q0 + i_tok) * p.Hq + h * p.G + (r - i_tok * p.G)) * D + threadIdx.x] =
+          round_out<OT>(o * inv);
+    }
+  }
+}
+
+// Warps and ring slots: as many page blocks as shared memory holds, and the
+// registers of the variant (9 warps: 168 a thread, 8 or 7: 255).
+template <int D, int NB>
+using LayoutOf =
+    std::conditional_t<D == 128, std::conditional_t<NB == 1, Layout<128, 8, 3>, Layout<128, 7, 3>>, Layout<256, 6, 2>>;
+
+template <int D, int NB, bool kSplit, typename QT, typename OT>
+cudaError_t launch_t(DeviceContext* ctx, Problem p, const void* q, void* out, cudaStream_t s, int* status) {
+  using L = LayoutOf<D, NB>;
+  p.max_rows = NB * (kSplit ? 4 : 8);
+  p.rows = p.max_rows;
+  const int64_t items = static_cast<int64_t>(p.c.num_seqs) * p.c.heads;
+  const int64_t most = items * p.c.max_pages;  // units at most
+  const int64_t grid = most < ctx->num_sms ? most : ctx->num_sms;
+  if (items > 0x7fffffff) return cudaErrorInvalidValue;
+  const size_t part = static_cast<size_t>(items + grid * L::kWarps) * p.rows * (D + 4) * 4;
+  uint8_t* ws = nullptr;
+  if ((*status = pool_alloc(ctx, reinterpret_cast<void**>(&ws), part + static_cast<size_t>(items) * 8, s)))
+    return cudaSuccess;
+  p.part = reinterpret_cast<float*>(ws);
+  p.ends = reinterpret_cast<int2*>(ws + part);
+  auto kern = k_kv4_decode<D, NB, kSplit, QT, OT, L>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (e == cudaSuccess) {
+    kern<<<static_cast<unsigned>(grid), L::kThreads, L::kBytes, s>>>(p, static_cast<const QT*>(q),
+                                                                     static_cast<OT*>(out));
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(items));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_kv4_join<D, OT>, static_cast<const Problem>(p), static_cast<OT*>(out));
+  }
+  pool_free(ws, s);
+  return e;
+}
+
+template <int D, typename QT, typename OT>
+cudaError_t launch_rows(DeviceContext* ctx, const Problem& p, int64_t rows, const void* q, void* out, cudaStream_t s,
+                        int* status) {
+  if (rows <= 4) return launch_t<D, 1, true, QT, OT>(ctx, p, q, out, s, status);
+  if constexpr (std::is_same<QT, float>::value) {
+    return launch_t<D, 2, true, QT, OT>(ctx, p, q, out, s, status);
+  } else {
+    if (rows <= 8) return launch_t<D, 1, false, QT, OT>(ctx, p, q, out, s, status);
+    return launch_t<D, 2, false, QT, OT>(ctx, p, q, out, s, status);
+  }
+}
+
+}  // namespace
+
+// Rows of an item that the kernel holds: 8 columns of 8 (16-bit) or 4 (fp32)
+// rows, two such blocks while the sums of a head of 128 fit the registers.
+bool kv4_decode_supported(int head_dim, int q_dtype, int64_t rows) {
+  const int per = q_dtype == BITNET_DTYPE_F32 ? 4 : 8;
+  return rows <= (head_dim == 128 ? 2 * per : per);
+}
+
+cudaError_t launch_kv4_decode(DeviceContext* ctx, const KvView& c, int head_dim, const void* q, int q_dtype, int64_t T,
+                              int Hq, int64_t rows, float scale, int causal, int window, void* out, int out_dtype,
+                              cudaStream_t s, int* status) {
+  Problem p = {};
+  p.c = c;
+  p.Hq = Hq;
+  p.G = Hq / c.heads;
+  p.T = static_cast<int>(T);
+  p.scale = scale * 1.4426950408889634f;
+  p.causal = causal;
+  p.window = window < (1 << 30) ? window : 1 << 30;  // keeps position - window within 32 bits
+  p.err = ctx->err_word;
+  auto go = [&](auto* qt, auto* ot) {
+    using QT = std::remove_pointer_t<decltype(qt)>;
+    using OT = std::remove_pointer_t<decltype(ot)>;
+    if (head_dim == 128) return launch_rows<128, QT, OT>(ctx, p, rows, q, out, s, status);
+    if constexpr (std::is_same<QT, float>::value) {
+      return launch_t<256, 1, true, QT, OT>(ctx, p, q, out, s, status);
+    } else {
+      return rows <= 4 ? launch_t<256, 1, true, QT, OT>(ctx, p, q, out, s, status)
+                       : launch_t<256, 1, false, QT, OT>(ctx, p, q, out, s, status);
+    }
+  };
+  float* f = nullptr;
+  __half* h = nullptr;
+  __nv_bfloat16* bf = nullptr;
+  const bool f32_out = out_dtype == BITNET_DTYPE_F32;
+  switch (q_dtype) {
+    case BITNET_DTYPE_F32: return go(f, f);
+    case BITNET_DTYPE_F16: return f32_out ? go(h, f) : go(h, h);
+    case BITNET_DTYPE_BF16: return f32_out ? go(bf, f) : go(bf, bf);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace bitnet
