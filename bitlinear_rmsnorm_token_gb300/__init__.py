@@ -34,6 +34,7 @@ ERR_NO_DEVICE = 6
 ERR_SCRATCH_LIMIT = 7
 ERR_BAD_INDEX = 8
 KV4_PAGE = 64
+_INT_MAX = (1 << 31) - 1  # bounds beyond it mean the same
 NOALLOC_SCRATCH_BYTES = 16 << 20
 FLAG_WEIGHTS_STATIC = 1
 MAX_GROUP = 16
@@ -414,19 +415,56 @@ def bitlinear_forward_group(group, M: int, eps: float = 1e-6, flags: int = 0, st
     _check(rc, "bitnet_bitlinear_forward_group")
 
 
-def _on_current_device(where, *tensors):
-    """The kernels run on the current device: tensors of another one are refused."""
+def _device(t, name):
+    """The current device's index, which t has to be on: the kernels run there."""
     import torch
 
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != here:
-            raise ValueError(f"{where}: a tensor is on {t.device}, the current device is cuda:{here}")
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        _dev(t, getattr(t, "dtype", None), name)  # says what is wrong
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _ptr(t, dtype, name, dev):
+    """Address of a contiguous tensor of `dtype` on device `dev`, as _dev checks it (a decode step makes a dozen of
+    these checks, so the passing case is kept short)."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name)
+    raise ValueError(f"{name} is on {t.device}, the other tensors are on cuda:{dev}")
+
+
+def _on(stream, dev):
+    """The stream's handle; default: the current stream of device `dev`."""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _shape(where, name, t, want):
-    if tuple(t.shape) != tuple(want):
+    if t.shape != want:
         raise ValueError(f"{where}: {name} must have the shape {tuple(want)}, got {tuple(t.shape)}")
+
+
+_DTYPE_CODES = None
+
+
+def _any_dtype(t, name):
+    """DTYPE_* of a float32, float16 or bfloat16 tensor."""
+    global _DTYPE_CODES
+    if _DTYPE_CODES is None:
+        import torch
+
+        _DTYPE_CODES = {torch.float32: DTYPE_F32, torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16}
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return code
 
 
 def quant_w8(w, codes=None, scale=None, stream=None):
@@ -435,20 +473,17 @@ def quant_w8(w, codes=None, scale=None, stream=None):
     import torch
 
     N, K = w.shape
+    dev = _device(w, "w")
     if codes is None:
         codes = torch.empty((N, K), dtype=torch.int8, device=w.device)
     if scale is None:
         scale = torch.empty(N, dtype=torch.float32, device=w.device)
     _shape("quant_w8", "codes", codes, (N, K))
     _shape("quant_w8", "scale", scale, (N,))
-    args = (_dev(w, torch.float32, "w"), N, K, _dev(codes, torch.int8, "codes"),
-            _dev(scale, torch.float32, "scale"))
-    _on_current_device("quant_w8", w, codes, scale)
-    _check(lib().bitnet_quant_w8(*args, _stream(stream)), "bitnet_quant_w8")
+    rc = lib().bitnet_quant_w8(_ptr(w, torch.float32, "w", dev), N, K, _ptr(codes, torch.int8, "codes", dev),
+                               _ptr(scale, torch.float32, "scale", dev), _on(stream, dev))
+    _check(rc, "bitnet_quant_w8")
     return codes, scale
-
-
-_ANY_DTYPE = (DTYPE_F32, DTYPE_F16, DTYPE_BF16)
 
 
 def w8a8_gemm(codes, a_scale, w_codes, w_scale, y=None, y_dtype=None, acc_out=None, stream=None):
@@ -458,20 +493,25 @@ def w8a8_gemm(codes, a_scale, w_codes, w_scale, y=None, y_dtype=None, acc_out=No
 
     M, K = codes.shape
     N = w_codes.shape[0]
-    if y is None:
-        y = torch.empty((M, N), dtype=y_dtype if y_dtype is not None else torch.float32, device=codes.device)
     _shape("w8a8_gemm", "a_scale", a_scale, (M,))
     _shape("w8a8_gemm", "w_codes", w_codes, (N, K))
     _shape("w8a8_gemm", "w_scale", w_scale, (N,))
-    _shape("w8a8_gemm", "y", y, (M, N))
+    if y is None:
+        y = torch.empty((M, N), dtype=y_dtype if y_dtype is not None else torch.float32, device=codes.device)
+    else:
+        _shape("w8a8_gemm", "y", y, (M, N))
+        if y_dtype is not None and y.dtype != y_dtype:
+            raise TypeError("w8a8_gemm: y and y_dtype differ")
     if acc_out is not None:
         _shape("w8a8_gemm", "acc_out", acc_out, (M, N))
-    yt = _dtype_code(y, "y", _ANY_DTYPE)
-    args = (_dev(codes, torch.int8, "codes"), _dev(a_scale, torch.float32, "a_scale"),
-            _dev(w_codes, torch.int8, "w_codes"), _dev(w_scale, torch.float32, "w_scale"), M, K, N,
-            _dev(y, y.dtype, "y"), yt, _opt(acc_out, torch.int32, "acc_out"))
-    _on_current_device("w8a8_gemm", codes, a_scale, w_codes, w_scale, y, acc_out)
-    _check(lib().bitnet_w8a8_gemm(*args, _stream(stream)), "bitnet_w8a8_gemm")
+    yt = _any_dtype(y, "y")
+    dev = _device(codes, "codes")
+    rc = lib().bitnet_w8a8_gemm(
+        _ptr(codes, torch.int8, "codes", dev), _ptr(a_scale, torch.float32, "a_scale", dev),
+        _ptr(w_codes, torch.int8, "w_codes", dev), _ptr(w_scale, torch.float32, "w_scale", dev), M, K, N,
+        _ptr(y, y.dtype, "y", dev), yt, None if acc_out is None else _ptr(acc_out, torch.int32, "acc_out", dev),
+        _on(stream, dev))
+    _check(rc, "bitnet_w8a8_gemm")
     return y
 
 
@@ -483,18 +523,23 @@ def w8a8_forward(x, norm_w, w_codes, w_scale, eps: float = 1e-6, y=None, y_dtype
 
     M, K = x.shape
     N = w_codes.shape[0]
-    if y is None:
-        y = torch.empty((M, N), dtype=y_dtype if y_dtype is not None else x.dtype, device=x.device)
+    xt = _any_dtype(x, "x")
     _shape("w8a8_forward", "norm_w", norm_w, (K,))
     _shape("w8a8_forward", "w_codes", w_codes, (N, K))
     _shape("w8a8_forward", "w_scale", w_scale, (N,))
-    _shape("w8a8_forward", "y", y, (M, N))
-    xt = _dtype_code(x, "x", _ANY_DTYPE)
-    yt = _dtype_code(y, "y", _ANY_DTYPE)
-    args = (_dev(x, x.dtype, "x"), xt, _dev(norm_w, torch.float32, "norm_w"), _dev(w_codes, torch.int8, "w_codes"),
-            _dev(w_scale, torch.float32, "w_scale"), M, K, N, float(eps), _dev(y, y.dtype, "y"), yt)
-    _on_current_device("w8a8_forward", x, norm_w, w_codes, w_scale, y)
-    _check(lib().bitnet_w8a8_forward(*args, _stream(stream)), "bitnet_w8a8_forward")
+    if y is None:
+        y = torch.empty((M, N), dtype=y_dtype if y_dtype is not None else x.dtype, device=x.device)
+    else:
+        _shape("w8a8_forward", "y", y, (M, N))
+        if y_dtype is not None and y.dtype != y_dtype:
+            raise TypeError("w8a8_forward: y and y_dtype differ")
+    yt = _any_dtype(y, "y")
+    dev = _device(x, "x")
+    rc = lib().bitnet_w8a8_forward(
+        _ptr(x, x.dtype, "x", dev), xt, _ptr(norm_w, torch.float32, "norm_w", dev),
+        _ptr(w_codes, torch.int8, "w_codes", dev), _ptr(w_scale, torch.float32, "w_scale", dev), M, K, N, eps,
+        _ptr(y, y.dtype, "y", dev), yt, _on(stream, dev))
+    _check(rc, "bitnet_w8a8_forward")
     return y
 
 
@@ -513,7 +558,7 @@ def kv4_cache(num_pages: int, num_kv_heads: int, head_dim: int, device="cuda"):
     return torch.empty((num_pages, num_kv_heads, kv4_block_bytes(head_dim)), dtype=torch.uint8, device=device)
 
 
-def _kv4(where, cache, num_kv_heads, head_dim, q_start, kv_lens, page_table):
+def _kv4(where, cache, num_kv_heads, head_dim, q_start, kv_lens, page_table, dev):
     import torch
 
     if page_table.dim() != 2:
@@ -521,12 +566,11 @@ def _kv4(where, cache, num_kv_heads, head_dim, q_start, kv_lens, page_table):
     B, most = page_table.shape
     _shape(where, "q_start", q_start, (B + 1,))
     _shape(where, "kv_lens", kv_lens, (B,))
-    if cache.dim() != 3 or cache.shape[1] != num_kv_heads or cache.shape[2] != 64 * head_dim + 16 * KV4_PAGE:
-        raise ValueError(f"{where}: cache must be [pages, {num_kv_heads}, {64 * head_dim + 16 * KV4_PAGE}], "
-                         f"got {tuple(cache.shape)}")
-    return Kv4(_dev(cache, torch.uint8, "cache"), cache.shape[0], num_kv_heads, head_dim,
-               _dev(q_start, torch.int32, "q_start"), _dev(kv_lens, torch.int32, "kv_lens"),
-               _dev(page_table, torch.int32, "page_table"), B, most)
+    pages = cache.shape[0] if cache.dim() else 0
+    _shape(where, "cache", cache, (pages, num_kv_heads, KV4_PAGE * (head_dim + 16)))
+    return Kv4(_ptr(cache, torch.uint8, "cache", dev), pages, num_kv_heads, head_dim,
+               _ptr(q_start, torch.int32, "q_start", dev), _ptr(kv_lens, torch.int32, "kv_lens", dev),
+               _ptr(page_table, torch.int32, "page_table", dev), B, most)
 
 
 def kv4_append(k, v, cache, q_start, kv_lens, page_table, stream=None):
@@ -538,11 +582,12 @@ def kv4_append(k, v, cache, q_start, kv_lens, page_table, stream=None):
     _shape("kv4_append", "v", v, k.shape)
     if v.dtype != k.dtype:
         raise TypeError("kv4_append: k and v differ in dtype")
-    t = _dtype_code(k, "k", _ANY_DTYPE)
-    c = _kv4("kv4_append", cache, H, D, q_start, kv_lens, page_table)
-    args = (_dev(k, k.dtype, "k"), _dev(v, v.dtype, "v"), t, T)
-    _on_current_device("kv4_append", k, v, cache, q_start, kv_lens, page_table)
-    _check(lib().bitnet_kv4_append(ctypes.byref(c), *args, _stream(stream)), "bitnet_kv4_append")
+    t = _any_dtype(k, "k")
+    dev = _device(k, "k")
+    c = _kv4("kv4_append", cache, H, D, q_start, kv_lens, page_table, dev)
+    rc = lib().bitnet_kv4_append(ctypes.byref(c), _ptr(k, k.dtype, "k", dev), _ptr(v, k.dtype, "v", dev), t, T,
+                                 _on(stream, dev))
+    _check(rc, "bitnet_kv4_append")
 
 
 def kv4_read(cache, T: int, num_kv_heads: int, head_dim: int, q_start, kv_lens, page_table, dtype=None, k=None, v=None,
@@ -560,11 +605,12 @@ def kv4_read(cache, T: int, num_kv_heads: int, head_dim: int, q_start, kv_lens, 
     _shape("kv4_read", "v", v, shape)
     if v.dtype != k.dtype or (dtype is not None and k.dtype != dtype):
         raise TypeError("kv4_read: k, v and dtype differ")
-    t = _dtype_code(k, "k", _ANY_DTYPE)
-    c = _kv4("kv4_read", cache, num_kv_heads, head_dim, q_start, kv_lens, page_table)
-    args = (T, _dev(k, k.dtype, "k"), _dev(v, v.dtype, "v"), t)
-    _on_current_device("kv4_read", k, v, cache, q_start, kv_lens, page_table)
-    _check(lib().bitnet_kv4_read(ctypes.byref(c), *args, _stream(stream)), "bitnet_kv4_read")
+    t = _any_dtype(k, "k")
+    dev = _device(cache, "cache")
+    c = _kv4("kv4_read", cache, num_kv_heads, head_dim, q_start, kv_lens, page_table, dev)
+    rc = lib().bitnet_kv4_read(ctypes.byref(c), T, _ptr(k, k.dtype, "k", dev), _ptr(v, k.dtype, "v", dev), t,
+                               _on(stream, dev))
+    _check(rc, "bitnet_kv4_read")
     return k, v
 
 
@@ -578,18 +624,22 @@ def kv4_attention(q, cache, num_kv_heads: int, q_start, kv_lens, page_table, max
     import torch
 
     T, Hq, D = q.shape
+    qt = _any_dtype(q, "q")
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype if out_dtype is not None else q.dtype, device=q.device)
-    _shape("kv4_attention", "out", out, q.shape)
-    if out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError("kv4_attention: out and out_dtype differ")
-    qt = _dtype_code(q, "q", _ANY_DTYPE)
-    ot = _dtype_code(out, "out", (qt, DTYPE_F32))
-    c = _kv4("kv4_attention", cache, num_kv_heads, D, q_start, kv_lens, page_table)
-    args = (_dev(q, q.dtype, "q"), qt, T, Hq, int(max_q_len), D ** -0.5 if scale is None else float(scale),
-            1 if causal else 0, int(window), _dev(out, out.dtype, "out"), ot)
-    _on_current_device("kv4_attention", q, cache, q_start, kv_lens, page_table, out)
-    _check(lib().bitnet_kv4_attention(ctypes.byref(c), *args, _stream(stream)), "bitnet_kv4_attention")
+        out = torch.empty_like(q, dtype=out_dtype)
+    else:
+        _shape("kv4_attention", "out", out, q.shape)
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError("kv4_attention: out and out_dtype differ")
+    ot = _any_dtype(out, "out")
+    if ot != qt and ot != DTYPE_F32:
+        raise TypeError(f"kv4_attention: out must be {q.dtype} or float32, got {out.dtype}")
+    dev = _device(q, "q")
+    c = _kv4("kv4_attention", cache, num_kv_heads, D, q_start, kv_lens, page_table, dev)
+    rc = lib().bitnet_kv4_attention(
+        ctypes.byref(c), _ptr(q, q.dtype, "q", dev), qt, T, Hq, min(max_q_len, _INT_MAX),
+        D ** -0.5 if scale is None else scale, 1 if causal else 0, min(window, _INT_MAX), _ptr(out, out.dtype, "out", dev), ot, _on(stream, dev))
+    _check(rc, "bitnet_kv4_attention")
     return out
 
 

@@ -1,6 +1,8 @@
 // api.cu -- the C ABI declared in include/bitnet.h: argument checks, dispatch
 // between the decode and tensor-core paths, per-device state.
 #include <mutex>
+#include <set>
+#include <utility>
 
 #include "common.cuh"
 #include "internal.h"
@@ -105,6 +107,16 @@ int pool_alloc(DeviceContext* ctx, void** p, size_t bytes, cudaStream_t stream) 
 
 void pool_free(void* p, cudaStream_t stream) {
   if (p) cudaFreeAsync(p, stream);
+}
+
+cudaError_t allow_smem(const DeviceContext* ctx, const void* kernel, int bytes) {
+  static std::mutex mu;
+  static std::set<std::pair<const void*, int>> done;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done.count({kernel, ctx->device})) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.insert({kernel, ctx->device});
+  return e;
 }
 
 EncodeTiledFn encode_tiled_fn() {

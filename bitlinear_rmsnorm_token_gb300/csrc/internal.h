@@ -30,6 +30,10 @@ int device_context_nopool(DeviceContext** ctx);
 int pool_alloc(DeviceContext* ctx, void** p, size_t bytes, cudaStream_t stream);
 void pool_free(void* p, cudaStream_t stream);
 
+// Lets `kernel` use `bytes` of dynamic shared memory on the context's device
+// (set once per kernel and device).
+cudaError_t allow_smem(const DeviceContext* ctx, const void* kernel, int bytes);
+
 // cuTensorMapEncodeTiled fetched through the runtime (no link to libcuda).
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,

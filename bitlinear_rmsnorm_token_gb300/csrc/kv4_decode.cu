@@ -97,9 +97,9 @@ struct Layout {
   static constexpr int kSlots = kWarps * kStages;
   static constexpr int offUnit = kSlots * KvBlock<D>::kBytes;
   static constexpr int offBar = offUnit + kSlots * static_cast<int>(sizeof(Unit));
-  static constexpr int offScan = offBar + 2 * kSlots * 8;
-  static constexpr int offMisc = offScan + kThreads * 4;  // per-warp sums, abort flag
-  static constexpr int kBytes = offMisc + 128;
+  static constexpr int offScan = offBar + 3 * kSlots * 8;
+  static constexpr int offMisc = offScan + kThreads * 4;  // per-warp sums (two sets), abort flag
+  static constexpr int kBytes = offMisc + 256;
   static_assert(kBytes <= 232448, "over the 227 KB of shared memory a CTA may use");
 };
 
@@ -145,60 +145,73 @@ __global__ void __launch_bounds__(L::kThreads, 1)
   constexpr int kCols = kSplit ? 1 : 2;      // scores per key, column block and lane
   extern __shared__ __align__(1024) uint8_t smem[];
   Unit* units = reinterpret_cast<Unit*>(smem + L::offUnit);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::offBar);
-  uint64_t* empty = full + L::kSlots;
-  int* scan = reinterpret_cast<int*>(smem + L::offScan);
-  int* misc = reinterpret_cast<int*>(smem + L::offMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 16);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::offBar);  // the page's bytes have landed
+  uint64_t* ready = full + L::kSlots;                              // its descriptor is written
+  uint64_t* empty = ready + L::kSlots;                             // the consumer is done with both
+  unsigned* scan = reinterpret_cast<unsigned*>(smem + L::offScan);
+  unsigned* misc = reinterpret_cast<unsigned*>(smem + L::offMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 32);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int B_seqs = p.c.num_seqs, H = p.c.heads;
+  const int B_seqs = p.c.num_seqs;
+  const unsigned H = p.c.heads;
   pdl_launch_dependents();
+  // ---- total pages (units fit 32 bits, checked on the host), then each producer lane finds where its warp's range
+  // begins: a running sum over the sequences, kThreads of them at a time
+  auto pages_of = [&](int b) -> unsigned {
+    int f, l, n, q0;
+    return b < B_seqs ? seq_pages(p, b, &f, &l, &n, &q0) : 0;
+  };
+  const unsigned pages0 = pages_of(threadIdx.x);
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(&full[i], 1);
+      mbar_init(&ready[i], 1);
       mbar_init(&empty[i], 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
   }
-  // ---- total pages, then the sequence where each warp's range begins
-  auto pages_of = [&](int b) {
-    int f, l, n, q0;
-    return b < B_seqs ? seq_pages(p, b, &f, &l, &n, &q0) : 0;
+  auto warp_scan = [&](unsigned x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
   };
-  int mine = 0;
-  for (int b = threadIdx.x; b < B_seqs; b += L::kThreads) mine += pages_of(b);
-  int s = warp_sum_int(mine);
-  if (lane == 0) misc[warp] = s;
+  unsigned mine = pages0;
+  for (int b = threadIdx.x + L::kThreads; b < B_seqs; b += L::kThreads) mine += pages_of(b);
+  const unsigned sum = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) misc[warp] = sum;
+  {
+    const unsigned x = warp_scan(pages0);
+    scan[threadIdx.x] = x;
+    if (lane == 31) misc[16 + warp] = x;
+  }
   __syncthreads();
-  int64_t total = 0;
+  unsigned total = 0;
   for (int w = 0; w <= kWarps; ++w) total += misc[w];
-  const int64_t U = total * H;
+  const unsigned U = total * H;
   // warp i of CTA c is number i * grid + c, so that few units spread over the CTAs; with fewer units than warps the
-  // first U warps take one each
-  const int64_t W = min(static_cast<int64_t>(gridDim.x) * kWarps, U);
+  // first U warps take one each.  Warp w takes uq or uq + 1 units, the first ur warps one more.
+  const unsigned W = min(gridDim.x * kWarps, U);
+  const unsigned uq = W ? U / W : 0, ur = W ? U - uq * W : 0;
   const int my_warp = warp < kWarps ? warp : lane;  // the producer's lanes: the warp that they serve
-  const int64_t w_me = static_cast<int64_t>(my_warp) * gridDim.x + blockIdx.x;
+  const unsigned w_me = my_warp * gridDim.x + blockIdx.x;
   const bool has = my_warp < kWarps && w_me < W;
-  const int64_t u0 = has ? U * w_me / W : 0, u1 = has ? U * (w_me + 1) / W : 0;
+  const unsigned u0 = w_me * uq + min(w_me, ur);
+  const unsigned count = has ? uq + (w_me < ur ? 1 : 0) : 0;
 
   if (warp < kWarps) {
-    // the scan below is the producer's; the consumers only take part in it
-    for (int c0 = 0; c0 < B_seqs; c0 += L::kThreads) {
-      const int v = pages_of(c0 + threadIdx.x);
-      int x = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
+    // further sequences: the producer searches, the consumers take part in the running sums
+    for (int c0 = L::kThreads; c0 < B_seqs; c0 += L::kThreads) {
+      const unsigned x = warp_scan(pages_of(c0 + threadIdx.x));
       __syncthreads();
       scan[threadIdx.x] = x;
-      if (lane == 31) misc[warp] = x;
+      if (lane == 31) misc[16 + warp] = x;
       __syncthreads();
     }
-    __syncthreads();
     // ------------------------------------------------------------ consumer
     const int g = lane >> 2, t = lane & 3;
     const int pg = g ^ ((g >> 1) & 1);  // key of tile row g: spreads the rows that lanes read together over the banks
@@ -206,10 +219,11 @@ __global__ void __launch_bounds__(L::kThreads, 1)
     float m_run[NB][kCols], l_run[NB][kCols], z_run[NB][kCols], qsum[NB][kCols], qc[NB][kCols];
     uint32_t qf[NB][kWordsK][4];
     int e_run = -100;
-    const int64_t count = u1 - u0;
-    for (int64_t k = 0; k < count; ++k) {
-      const int slot = warp * kStages + static_cast<int>(k % kStages);
-      if (!mbar_wait(&full[slot], static_cast<unsigned>((k / kStages) & 1), p.err, abort_flag)) break;
+    int stage = 0;
+    unsigned phase = 0;
+    for (unsigned k = 0; k < count; ++k) {
+      const int slot = warp * kStages + stage;
+      if (!mbar_wait(&ready[slot], phase, p.err, abort_flag)) break;
       const Unit un = units[slot];
       const uint8_t* blk = smem + slot * B::kBytes;
       const int rows = un.n * p.G;
@@ -279,6 +293,11 @@ __global__ void __launch_bounds__(L::kThreads, 1)
             z_run[nb][j] = 0.0f;
           }
         }
+      }
+      if (!mbar_wait(&full[slot], phase, p.err, abort_flag)) break;
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
       }
       if (un.flags & kValid) {
         // ---- scores of the page's 64 keys: tile kt, rows g and g + 8
@@ -504,7 +523,7 @@ __global__ void __launch_bounds__(L::kThreads, 1)
                 reinterpret_cast<uint4*>(dst)[i] = pk.u;
               }
             } else {
-              float* dst = p.part + ((un.item + w_me) * p.rows + r) * (D + 4);
+              float* dst = p.part + ((static_cast<int64_t>(un.item) + w_me) * p.rows + r) * (D + 4);
 #pragma unroll
               for (int i = 0; i < kTiles / 2; ++i)
                 reinterpret_cast<float4*>(dst + 2 * kTiles * g)[i] =
@@ -517,51 +536,47 @@ __global__ void __launch_bounds__(L::kThreads, 1)
   } else {
     // ------------------------------------------------------------ producer
     int b = 0;
-    int64_t base = 0, before = 0;  // pages before the chunk, and before sequence b
+    unsigned base = 0, before = 0;  // pages before the chunk, and before sequence b
     for (int c0 = 0; c0 < B_seqs; c0 += L::kThreads) {
-      const int v = pages_of(c0 + threadIdx.x);
-      int x = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+      if (c0 > 0) {
+        const unsigned x = warp_scan(pages_of(c0 + threadIdx.x));
+        __syncthreads();
+        scan[threadIdx.x] = x;
+        if (lane == 31) misc[16 + warp] = x;
+        __syncthreads();
       }
-      __syncthreads();
-      scan[threadIdx.x] = x;
-      if (lane == 31) misc[warp] = x;
-      __syncthreads();
-      const int64_t want = u0 / H - base;  // page of the chunk where the range begins
-      int64_t chunk = 0;
+      const unsigned want = u0 / H;  // the page where the range begins
       for (int w = 0; w <= kWarps; ++w) {
-        const int64_t in = misc[w];
-        if (u0 < u1 && want >= chunk && want < chunk + in) {
-          int i = 0;  // first of the warp's 32 sequences whose running sum passes it
-          while (scan[32 * w + i] <= want - chunk) ++i;
+        const unsigned in = misc[16 + w];
+        if (count > 0 && want >= base && want < base + in) {
+          int i = 0;  // the first of the warp's 32 sequences whose running sum passes it
+          for (int o = 16; o; o >>= 1)
+            if (scan[32 * w + i + o - 1] <= want - base) i += o;
           b = c0 + 32 * w + i;
-          before = base + chunk + (i ? scan[32 * w + i - 1] : 0);
+          before = base + (i ? scan[32 * w + i - 1] : 0);
         }
-        chunk += in;
+        base += in;
       }
-      base += chunk;
     }
-    __syncthreads();
     if (lane < kWarps) {
-      int first = 0, len = 0, n = 0, q0 = 0, pages = 0, h = 0, pg = 0;
-      if (u0 < u1) {
+      int first = 0, len = 0, n = 0, q0 = 0;
+      unsigned pages = 0, h = 0, pg = 0;
+      if (count > 0) {
         pages = seq_pages(p, b, &first, &len, &n, &q0);
-        const int64_t o = u0 - before * H;
-        h = static_cast<int>(o / pages);
-        pg = static_cast<int>(o - static_cast<int64_t>(h) * pages);
+        const unsigned o = u0 - before * H;
+        h = o / pages;
+        pg = o - h * pages;
       }
-      const int64_t count = u1 - u0;
-      bool fresh = true;  // the segment's first page
-      int64_t seg0 = 0;   // and its place in the range
-      int64_t k = 0;
+      bool fresh = true;    // the segment's first page
+      unsigned seg0 = 0;    // and its place in the range
+      unsigned k = 0;
+      int stage = 0;
+      unsigned phase = 1;
       // The lanes poll without blocking, each going on as soon as its own warp has freed a slot.
       unsigned long long since = global_timer_ns();
       while (k < count) {
-        const int slot = lane * kStages + static_cast<int>(k % kStages);
-        if (!mbar_test(&empty[slot], static_cast<unsigned>((k / kStages) & 1) ^ 1u)) {
+        const int slot = lane * kStages + stage;
+        if (!mbar_test(&empty[slot], phase)) {
           if (*abort_flag) break;
           if (global_timer_ns() - since > kWaitTimeoutNs) {
             atomicOr(p.err, kErrWaitTimeout);
@@ -571,24 +586,11 @@ __global__ void __launch_bounds__(L::kThreads, 1)
           __nanosleep(40);
           continue;
         }
-        const int page_i = first + pg;
+        const int page_i = first + static_cast<int>(pg);
         int page = -1;
-        if (len > 0) {
-          page = p.c.page_table[static_cast<int64_t>(b) * p.c.max_pages + page_i];
-          if (page < 0 || page >= p.c.num_pages) {
-            page = -1;
-            atomicOr(p.err, kErrBadIndex);
-          }
-        }
-        if (fresh) {
-          seg0 = k;
-          if (pg == 0) {  // this range holds the item's beginning: say where it ends
-            const int64_t z = u0 + k + pages - 1;
-            p.ends[static_cast<int64_t>(b) * H + h] =
-                make_int2(static_cast<int>(w_me), static_cast<int>(((z + 1) * W - 1) / U));
-          }
-        }
+        if (len > 0) page = p.c.page_table[static_cast<int64_t>(b) * p.c.max_pages + page_i];
         const bool last_of_item = pg == pages - 1;
+        if (fresh) seg0 = k;
         Unit un;
         un.key0 = page_i * kKvPage;
         un.len = len;
@@ -596,16 +598,26 @@ __global__ void __launch_bounds__(L::kThreads, 1)
         un.q0 = q0;
         un.head = h;
         un.item = b * H + h;
+        un.pad = 0;
+        if (page < 0 || page >= p.c.num_pages) {
+          if (len > 0) atomicOr(p.err, kErrBadIndex);
+          page = -1;
+        }
         un.flags = (page >= 0 ? kValid : 0) | (fresh ? kFirst : 0) | (last_of_item || k == count - 1 ? kLast : 0) |
                    (last_of_item && k - seg0 == pages - 1 ? kWhole : 0);
-        un.pad = 0;
         units[slot] = un;
+        mbar_arrive(&ready[slot]);
         if (page >= 0) {
           mbar_arrive_expect_tx(&full[slot], B::kBytes);
           bulk_load(smem + slot * B::kBytes, p.c.cache + (static_cast<int64_t>(page) * H + h) * B::kBytes, B::kBytes,
                     &full[slot]);
         } else {
           mbar_arrive(&full[slot]);
+        }
+        if (fresh && pg == 0) {  // this range holds the item's beginning: say which warp holds its end
+          const unsigned z = u0 + k + pages - 1, wide = ur * (uq + 1);
+          p.ends[un.item] = make_int2(static_cast<int>(w_me),
+                                      static_cast<int>(z < wide ? z / (uq + 1) : ur + (z - wide) / uq));
         }
         since = global_timer_ns();
         fresh = last_of_item;
@@ -620,58 +632,85 @@ __global__ void __launch_bounds__(L::kThreads, 1)
           }
         }
         ++k;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
       if (*abort_flag)  // given up: copies still in flight must land before the CTA's shared memory goes
-        for (int64_t i = max(static_cast<int64_t>(0), k - kStages); i < k; ++i)
-          mbar_wait(&full[lane * kStages + static_cast<int>(i % kStages)], static_cast<unsigned>((i / kStages) & 1), p.err);
+        for (unsigned i = k > kStages ? k - kStages : 0; i < k; ++i)
+          mbar_wait(&full[lane * kStages + i % kStages], (i / kStages) & 1, p.err);
     }
   }
 }
 
-// Joins the segments of the items that several warps shared: one CTA per item,
-// a thread per output element, segments in order.
+// Joins the segments of the items that several warps shared, in order: a warp
+// per (item, row), 32 segments' maxima and sums at a time.
+constexpr int kJoinWarps = 4;
+
 template <int D, typename OT>
-__global__ void __launch_bounds__(256) k_kv4_join(const Problem p, OT* __restrict__ out) {
-  __shared__ float s_f[64];
-  pdl_wait();
-  const int item = blockIdx.x, b = item / p.c.heads, h = item - b * p.c.heads;
+__global__ void __launch_bounds__(kJoinWarps * 32) k_kv4_join(const Problem p, OT* __restrict__ out) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  const int64_t item = w / p.rows;
+  const int r = static_cast<int>(w - item * p.rows);
+  if (item >= static_cast<int64_t>(p.c.num_seqs) * p.c.heads) return;
+  const int b = static_cast<int>(item / p.c.heads), h = static_cast<int>(item - static_cast<int64_t>(b) * p.c.heads);
   const int q0 = p.c.q_start[b], n = p.c.q_start[b + 1] - q0;
+  pdl_wait();
   if (n <= 0 || q0 < 0 || static_cast<int64_t>(q0) + n > p.T || static_cast<int64_t>(n) * p.G > p.max_rows) return;
+  if (r >= n * p.G) return;
   const int2 e = p.ends[item];
   if (e.x == e.y) return;
   const int segs = e.y - e.x + 1;
-  const float* part = p.part + (static_cast<int64_t>(item) + e.x) * p.rows * (D + 4);
   const int64_t stride = static_cast<int64_t>(p.rows) * (D + 4);
-  const int rows = n * p.G;
-  for (int r = 0; r < rows; ++r) {
-    const float* pr = part + static_cast<int64_t>(r) * (D + 4);
-    float m = -INFINITY;
-    for (int i = threadIdx.x & 31; i < segs; i += 32) m = fmaxf(m, pr[i * stride + D]);
+  const float* part = p.part + (item + e.x) * stride + static_cast<int64_t>(r) * (D + 4);
+  float o[kPer], m = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m == -INFINITY) m = 0.0f;
-    float o = 0.0f, l = 0.0f;
-    for (int i0 = 0; i0 < segs; i0 += 64) {
-      __syncthreads();
-      const int i = i0 + threadIdx.x;
-      if (threadIdx.x < 64) s_f[threadIdx.x] = i < segs ? ex2(pr[i * stride + D] - m) : 0.0f;
-      __syncthreads();
-      const int most = min(64, segs - i0);
-      if (threadIdx.x < D) {
-        const float* src = pr + i0 * stride;
+  for (int i = 0; i < kPer; ++i) o[i] = 0.0f;
+  for (int i0 = 0; i0 < segs; i0 += 32) {
+    const bool on = i0 + lane < segs;
+    const float2 ml = on ? *reinterpret_cast<const float2*>(part + (i0 + lane) * stride + D)
+                         : make_float2(-INFINITY, 0.0f);
+    float m2 = ml.x;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, k));
+    m2 = fmaxf(m, m2);
+    const float ref = m2 == -INFINITY ? 0.0f : m2;
+    const float f_old = ex2(m - ref), f = ex2(ml.x - ref);
+    m = m2;
+    float ls = f * ml.y;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, k);
+    l = l * f_old + ls;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[i] *= f_old;
+    const int most = min(32, segs - i0);
 #pragma unroll 8
-        for (int j = 0; j < most; ++j) {
-          o = fmaf(s_f[j], src[j * stride + threadIdx.x], o);
-          l = fmaf(s_f[j], src[j * stride + D + 1], l);
-        }
+    for (int j = 0; j < most; ++j) {
+      const float fj = __shfl_sync(0xffffffffu, f, j);
+      const float4* src = reinterpret_cast<const float4*>(part + (i0 + j) * stride) + lane;
+#pragma unroll
+      for (int i = 0; i < kPer / 4; ++i) {
+        const float4 v = src[32 * i];
+        o[4 * i] = fmaf(fj, v.x, o[4 * i]);
+        o[4 * i + 1] = fmaf(fj, v.y, o[4 * i + 1]);
+        o[4 * i + 2] = fmaf(fj, v.z, o[4 * i + 2]);
+        o[4 * i + 3] = fmaf(fj, v.w, o[4 * i + 3]);
       }
     }
-    if (threadIdx.x < D) {
-      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-      const int i_tok = r / p.G;
-      out[(static_cast<int64_t>(q0 + i_tok) * p.Hq + h * p.G + (r - i_tok * p.G)) * D + threadIdx.x] =
-          round_out<OT>(o * inv);
-    }
+  }
+  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // no key seen: zeros; NaN stays
+  const int i_tok = r / p.G;
+  OT* dst = out + (static_cast<int64_t>(q0 + i_tok) * p.Hq + h * p.G + (r - i_tok * p.G)) * D;
+#pragma unroll
+  for (int i = 0; i < kPer / 4; ++i) {
+    union { OT v[4]; uint2 u2; uint4 u4; } pk;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) pk.v[c] = round_out<OT>(o[4 * i + c] * inv);
+    if constexpr (sizeof(OT) == 4) *reinterpret_cast<uint4*>(dst + 128 * i + 4 * lane) = pk.u4;
+    else *reinterpret_cast<uint2*>(dst + 128 * i + 4 * lane) = pk.u2;
   }
 }
 
@@ -682,14 +721,18 @@ using LayoutOf =
     std::conditional_t<D == 128, std::conditional_t<NB == 1, Layout<128, 8, 3>, Layout<128, 7, 3>>, Layout<256, 6, 2>>;
 
 template <int D, int NB, bool kSplit, typename QT, typename OT>
-cudaError_t launch_t(DeviceContext* ctx, Problem p, const void* q, void* out, cudaStream_t s, int* status) {
+cudaError_t launch_t(DeviceContext* ctx, Problem p, int64_t rows, const void* q, void* out, cudaStream_t s,
+                     int* status) {
   using L = LayoutOf<D, NB>;
-  p.max_rows = NB * (kSplit ? 4 : 8);
-  p.rows = p.max_rows;
+  p.max_rows = static_cast<int>(rows);
+  p.rows = static_cast<int>(rows);
   const int64_t items = static_cast<int64_t>(p.c.num_seqs) * p.c.heads;
   const int64_t most = items * p.c.max_pages;  // units at most
   const int64_t grid = most < ctx->num_sms ? most : ctx->num_sms;
-  if (items > 0x7fffffff) return cudaErrorInvalidValue;
+  if (most > 0x7fffffff) {  // units are counted in 32 bits
+    *status = BITNET_ERR_UNSUPPORTED_SHAPE;
+    return cudaSuccess;
+  }
   const size_t part = static_cast<size_t>(items + grid * L::kWarps) * p.rows * (D + 4) * 4;
   uint8_t* ws = nullptr;
   if ((*status = pool_alloc(ctx, reinterpret_cast<void**>(&ws), part + static_cast<size_t>(items) * 8, s)))
@@ -697,7 +740,7 @@ cudaError_t launch_t(DeviceContext* ctx, Problem p, const void* q, void* out, cu
   p.part = reinterpret_cast<float*>(ws);
   p.ends = reinterpret_cast<int2*>(ws + part);
   auto kern = k_kv4_decode<D, NB, kSplit, QT, OT, L>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  cudaError_t e = allow_smem(ctx, reinterpret_cast<const void*>(kern), L::kBytes);
   if (e == cudaSuccess) {
     kern<<<static_cast<unsigned>(grid), L::kThreads, L::kBytes, s>>>(p, static_cast<const QT*>(q),
                                                                      static_cast<OT*>(out));
@@ -705,8 +748,8 @@ cudaError_t launch_t(DeviceContext* ctx, Problem p, const void* q, void* out, cu
   }
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(items));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(static_cast<unsigned>((items * p.rows + kJoinWarps - 1) / kJoinWarps));
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -722,12 +765,12 @@ cudaError_t launch_t(DeviceContext* ctx, Problem p, const void* q, void* out, cu
 template <int D, typename QT, typename OT>
 cudaError_t launch_rows(DeviceContext* ctx, const Problem& p, int64_t rows, const void* q, void* out, cudaStream_t s,
                         int* status) {
-  if (rows <= 4) return launch_t<D, 1, true, QT, OT>(ctx, p, q, out, s, status);
+  if (rows <= 4) return launch_t<D, 1, true, QT, OT>(ctx, p, rows, q, out, s, status);
   if constexpr (std::is_same<QT, float>::value) {
-    return launch_t<D, 2, true, QT, OT>(ctx, p, q, out, s, status);
+    return launch_t<D, 2, true, QT, OT>(ctx, p, rows, q, out, s, status);
   } else {
-    if (rows <= 8) return launch_t<D, 1, false, QT, OT>(ctx, p, q, out, s, status);
-    return launch_t<D, 2, false, QT, OT>(ctx, p, q, out, s, status);
+    if (rows <= 8) return launch_t<D, 1, false, QT, OT>(ctx, p, rows, q, out, s, status);
+    return launch_t<D, 2, false, QT, OT>(ctx, p, rows, q, out, s, status);
   }
 }
 
@@ -757,10 +800,10 @@ cudaError_t launch_kv4_decode(DeviceContext* ctx, const KvView& c, int head_dim,
     using OT = std::remove_pointer_t<decltype(ot)>;
     if (head_dim == 128) return launch_rows<128, QT, OT>(ctx, p, rows, q, out, s, status);
     if constexpr (std::is_same<QT, float>::value) {
-      return launch_t<256, 1, true, QT, OT>(ctx, p, q, out, s, status);
+      return launch_t<256, 1, true, QT, OT>(ctx, p, rows, q, out, s, status);
     } else {
-      return rows <= 4 ? launch_t<256, 1, true, QT, OT>(ctx, p, q, out, s, status)
-                       : launch_t<256, 1, false, QT, OT>(ctx, p, q, out, s, status);
+      return rows <= 4 ? launch_t<256, 1, true, QT, OT>(ctx, p, rows, q, out, s, status)
+                       : launch_t<256, 1, false, QT, OT>(ctx, p, rows, q, out, s, status);
     }
   };
   float* f = nullptr;
