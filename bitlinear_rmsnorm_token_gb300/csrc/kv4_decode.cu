@@ -19,19 +19,20 @@
 // 16-row side and the query rows as the 8-column side: a page is read once for
 // all rows of its item, and the work stays far below what feeding it costs
 // (tcgen05 would take a 128-row tile for these 8 columns).
-//   S^T[64 keys, cols] = C_k q^T:  the 4-bit codes themselves are the operand.
-//     A code masked out of its word is the fp16 subnormal c 2^-24 (or 16 c 2^-24
-//     from the higher nibble, met by q / 16): one AND per two codes.
-//     q . k_j = s_j (q . c_j) + m_j sum(q).
-//   O^T[D, cols] = C_v^T W:  W = p_j s_j as fp16, the same encoding of c_j, pairs
-//     of keys put side by side by a byte permute.  sum p_j m_j is a scalar per
-//     row.  W is kept in fp16's range by a power of two of the largest s_j met.
+//   S^T[64 keys, cols] = C_k q^T:  the codes, as c - 8, are the fp16 operand: two
+//     codes at a time masked into the mantissa of 1024 (or 16 times as large, from
+//     the higher nibble) and moved to -8 .. 7 by one fma, exactly.
+//     q . k_j = s_j (q . (c_j - 8)) + (m_j + 8 s_j) sum(q).
+//   O^T[D, cols] = C_v^T W:  W = p_j s_j as fp16, the same operand of c_j - 8, pairs
+//     of keys put side by side by a byte permute.  sum p_j (m_j + 8 s_j) is a scalar
+//     per row.  W is kept in fp16's range by a power of two of the largest s_j met.
+//     Without the -8 (subnormal fp16 codes, one AND and no fma) the two terms are
+//     large and cancel, and the tensor core truncates its running sum: 1e-4 of the
+//     result over 4096 keys, measured.
 // Queries are scaled by a power of two per row.  fp32 queries are two fp16
 // parts in neighbouring columns (hi, lo: 22 bits), as is W then; a 16-bit query
-// is one fp16 exactly, and W takes two parts whenever the columns suffice.
-// With one part (2^-11), the error that rounding W makes at the middle of a
-// row's range (code 7.5) is added back as part of the scalar, which leaves what
-// rounding probabilities against centred values would.
+// is one fp16 exactly, and W takes two parts whenever the columns suffice (one
+// part rounds a probability by up to 2^-11).
 #include <type_traits>
 
 #include "common.cuh"
@@ -65,6 +66,21 @@ __device__ __forceinline__ uint32_t movm(uint32_t a) {
   return d;
 }
 
+// Codes in bits 0-3 (4-7) of both halves of w, other bits ignored, to fp16 c - 8.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
+  const uint32_t x = (w & 0x000f000fu) | 0x64006400u;  // 1024 + c
+  const uint32_t k = 0x64086408u;                      // 1032
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
+  const uint32_t x = (w & 0x00f000f0u) | 0x64006400u;        // 1024 + 16 c
+  const uint32_t k = 0x2c002c00u, m = 0xd480d480u;           // 1/16, -72
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&k),
+                            *reinterpret_cast<const __half2*>(&m));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 __device__ __forceinline__ uint32_t pack_h2(__half a, __half b) {
   return static_cast<uint32_t>(__half_as_ushort(a)) | (static_cast<uint32_t>(__half_as_ushort(b)) << 16);
 }
@@ -87,7 +103,13 @@ struct __align__(16) Unit {
   int item;    // sequence * heads + head
   int pad;
 };
-constexpr int kValid = 1, kFirst = 2, kLast = 4, kWhole = 8;
+constexpr int kValid = 1, kFirst = 2, kLast = 4, kWhole = 8, kStop = 16;
+
+// What an item costs besides its pages (queries in, result out), in pages: the
+// ranges are equal in pages + kItemCost.  Without it a warp that is dealt many
+// short items ends late (64 sequences of 1 .. 8192 tokens, 8 heads: the last warp
+// at 58 us, nine in ten by 46 us).
+constexpr unsigned kItemCost = 1;
 
 template <int D, int kWarps_, int kStages_>
 struct Layout {
@@ -98,7 +120,8 @@ struct Layout {
   static constexpr int offUnit = kSlots * KvBlock<D>::kBytes;
   static constexpr int offBar = offUnit + kSlots * static_cast<int>(sizeof(Unit));
   static constexpr int offScan = offBar + 3 * kSlots * 8;
-  static constexpr int offMisc = offScan + kThreads * 4;  // per-warp sums (two sets), abort flag
+  static constexpr int offSeq = (offScan + kThreads * 4 + 15) / 16 * 16;  // plan of the first kThreads sequences
+  static constexpr int offMisc = offSeq + kThreads * 16;  // per-warp sums (two sets), abort flag
   static constexpr int kBytes = offMisc + 256;
   static_assert(kBytes <= 232448, "over the 227 KB of shared memory a CTA may use");
 };
@@ -156,13 +179,21 @@ __global__ void __launch_bounds__(L::kThreads, 1)
   const int B_seqs = p.c.num_seqs;
   const unsigned H = p.c.heads;
   pdl_launch_dependents();
-  // ---- total pages (units fit 32 bits, checked on the host), then each producer lane finds where its warp's range
+  // ---- total work (it fits 32 bits, checked on the host), then each producer lane finds where its warp's range
   // begins: a running sum over the sequences, kThreads of them at a time
-  auto pages_of = [&](int b) -> unsigned {
+  int4* seqs = reinterpret_cast<int4*>(smem + L::offSeq);  // first page, length, rows, first row
+  auto work_of = [&](int b) -> unsigned {
     int f, l, n, q0;
-    return b < B_seqs ? seq_pages(p, b, &f, &l, &n, &q0) : 0;
+    const unsigned pages = b < B_seqs ? seq_pages(p, b, &f, &l, &n, &q0) : 0;
+    return pages ? pages + kItemCost : 0;
   };
-  const unsigned pages0 = pages_of(threadIdx.x);
+  unsigned work0 = 0;
+  if (static_cast<int>(threadIdx.x) < B_seqs) {
+    int4 v = make_int4(0, 0, 0, 0);
+    work0 = seq_pages(p, threadIdx.x, &v.x, &v.y, &v.z, &v.w);
+    if (work0) work0 += kItemCost;
+    seqs[threadIdx.x] = v;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(&full[i], 1);
@@ -180,12 +211,12 @@ __global__ void __launch_bounds__(L::kThreads, 1)
     }
     return x;
   };
-  unsigned mine = pages0;
-  for (int b = threadIdx.x + L::kThreads; b < B_seqs; b += L::kThreads) mine += pages_of(b);
+  unsigned mine = work0;
+  for (int b = threadIdx.x + L::kThreads; b < B_seqs; b += L::kThreads) mine += work_of(b);
   const unsigned sum = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0) misc[warp] = sum;
   {
-    const unsigned x = warp_scan(pages0);
+    const unsigned x = warp_scan(work0);
     scan[threadIdx.x] = x;
     if (lane == 31) misc[16 + warp] = x;
   }
@@ -201,12 +232,12 @@ __global__ void __launch_bounds__(L::kThreads, 1)
   const unsigned w_me = my_warp * gridDim.x + blockIdx.x;
   const bool has = my_warp < kWarps && w_me < W;
   const unsigned u0 = w_me * uq + min(w_me, ur);
-  const unsigned count = has ? uq + (w_me < ur ? 1 : 0) : 0;
+  const unsigned u1 = has ? u0 + uq + (w_me < ur ? 1 : 0) : 0;  // 0: nothing to do
 
   if (warp < kWarps) {
     // further sequences: the producer searches, the consumers take part in the running sums
     for (int c0 = L::kThreads; c0 < B_seqs; c0 += L::kThreads) {
-      const unsigned x = warp_scan(pages_of(c0 + threadIdx.x));
+      const unsigned x = warp_scan(work_of(c0 + threadIdx.x));
       __syncthreads();
       scan[threadIdx.x] = x;
       if (lane == 31) misc[16 + warp] = x;
@@ -221,10 +252,11 @@ __global__ void __launch_bounds__(L::kThreads, 1)
     int e_run = -100;
     int stage = 0;
     unsigned phase = 0;
-    for (unsigned k = 0; k < count; ++k) {
+    for (;;) {
       const int slot = warp * kStages + stage;
       if (!mbar_wait(&ready[slot], phase, p.err, abort_flag)) break;
       const Unit un = units[slot];
+      if (un.flags & kStop) break;
       const uint8_t* blk = smem + slot * B::kBytes;
       const int rows = un.n * p.G;
       if (un.flags & kFirst) {
@@ -267,24 +299,20 @@ __global__ void __launch_bounds__(L::kThreads, 1)
           }
 #pragma unroll
           for (int w = 0; w < kWordsK; ++w) {
-            const __half inv16 = __float2half_rn(0.0625f);
-            const __half* x = h + 8 * w;
-            qf[nb][w][0] = pack_h2(x[0], x[4]);
-            qf[nb][w][1] = pack_h2(__hmul(x[1], inv16), __hmul(x[5], inv16));
-            qf[nb][w][2] = pack_h2(x[2], x[6]);
-            qf[nb][w][3] = pack_h2(__hmul(x[3], inv16), __hmul(x[7], inv16));
+            // nibbles i and i + 4 of a word come side by side
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qf[nb][w][i] = pack_h2(h[8 * w + i], h[8 * w + i + 4]);
           }
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
           // to the lanes that hold the scores of these columns: 2t and 2t + 1
           const float s0 = __shfl_sync(0xffffffffu, sum, 8 * t), s1 = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
           const int e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
-          // S comes in units of 2^-24: sum(q) likewise, undone with the row's power of two in qc
-          qsum[nb][0] = (kSplit ? s0 + s1 : s0) * 0x1p-24f;
-          qc[nb][0] = p.scale * pow2(e0 - 14) * 0x1p24f;
+          qsum[nb][0] = kSplit ? s0 + s1 : s0;
+          qc[nb][0] = p.scale * pow2(e0 - 14);  // undoes the row's power of two
           if constexpr (!kSplit) {
-            qsum[nb][1] = s1 * 0x1p-24f;
-            qc[nb][1] = p.scale * pow2(e1 - 14) * 0x1p24f;
+            qsum[nb][1] = s1;
+            qc[nb][1] = p.scale * pow2(e1 - 14);
           }
 #pragma unroll
           for (int j = 0; j < kCols; ++j) {
@@ -317,12 +345,13 @@ __global__ void __launch_bounds__(L::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t ah = wa[i] >> 8, bh = wb[i] >> 8;
+              const uint32_t a0 = codes_lo(wa[i]), a1 = codes_lo(wb[i]), a2 = codes_hi(wa[i]), a3 = codes_hi(wb[i]);
+              const uint32_t c0 = codes_lo(ah), c1 = codes_lo(bh), c2 = codes_hi(ah), c3 = codes_hi(bh);
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
                 const uint32_t* f = qf[nb][4 * c + i];
-                mma16816(sc[nb][kt], wa[i] & 0x000f000fu, wb[i] & 0x000f000fu, wa[i] & 0x00f000f0u, wb[i] & 0x00f000f0u,
-                         f[0], f[1]);
-                mma16816(sc[nb][kt], ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u, bh & 0x00f000f0u, f[2], f[3]);
+                mma16816(sc[nb][kt], a0, a1, a2, a3, f[0], f[1]);
+                mma16816(sc[nb][kt], c0, c1, c2, c3, f[2], f[3]);
               }
             }
           }
@@ -343,8 +372,9 @@ __global__ void __launch_bounds__(L::kThreads, 1)
         for (int i = 0; i < 8; ++i) {
           const int key = 16 * (i >> 1) + 8 * (i & 1) + pg;
           const float2 km = kmeta[key], vv = vmeta[key];
+          const float kmid = fmaf(8.0f, km.x, km.y);  // what code 8 stands for
           vs[i] = vv.x;
-          vm[i] = vv.y;
+          vm[i] = fmaf(8.0f, vv.x, vv.y);
           if (!inner && un.key0 + key >= un.len) vs[i] = vm[i] = 0.0f;  // a slot without a token: any bytes
           smax = fmaxf(smax, vs[i]);
 #pragma unroll
@@ -353,7 +383,7 @@ __global__ void __launch_bounds__(L::kThreads, 1)
             for (int j = 0; j < kCols; ++j) {
               const float* s4 = sc[nb][i >> 1] + 2 * (i & 1);
               const float dot = kSplit ? s4[0] + s4[1] : s4[j];
-              x[nb][i][j] = fmaf(dot, km.x, km.y * qsum[nb][j]) * qc[nb][j];
+              x[nb][i][j] = fmaf(dot, km.x, kmid * qsum[nb][j]) * qc[nb][j];
             }
           }
         }
@@ -418,7 +448,6 @@ __global__ void __launch_bounds__(L::kThreads, 1)
         }
         // ---- probabilities, their sums, and W as B fragments
         const float vf = pow2(14 - e_run);
-        [[maybe_unused]] const float mid = 7.5f * pow2(e_run - 14);
         uint32_t wf[NB][4][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -434,17 +463,9 @@ __global__ void __launch_bounds__(L::kThreads, 1)
               const float pr = ex2(x[nb][i][j] - mref[j]);
               const float w = none ? 0.0f : pr * (vs[i] * vf);
               l_run[nb][j] += pr;
-              const __half h = __float2half_rn(w);
-              const float rest = w - __half2float(h);
-              float zi = none ? 0.0f : pr * vm[i];
-              if constexpr (kSplit) {
-                hw[0] = h;
-                hw[1] = __float2half_rn(rest);
-              } else {
-                hw[j] = h;
-                zi = fmaf(rest, mid, zi);
-              }
-              z_run[nb][j] += zi;
+              hw[j] = __float2half_rn(w);
+              if constexpr (kSplit) hw[1] = __float2half_rn(w - __half2float(hw[0]));
+              z_run[nb][j] += none ? 0.0f : pr * vm[i];
             }
             wf[nb][i >> 1][i & 1] = movm(pack_h2(hw[0], hw[1]));
           }
@@ -477,10 +498,9 @@ __global__ void __launch_bounds__(L::kThreads, 1)
             const uint32_t sel = (i & 3) | ((4 + (i & 3)) << 8);
             const uint32_t a = prmt_b32(w[0][i >> 2], w[1][i >> 2], sel);
             const uint32_t b = prmt_b32(w[2][i >> 2], w[3][i >> 2], sel);
+            const uint32_t a0 = codes_lo(a), a1 = codes_hi(a), a2 = codes_lo(b), a3 = codes_hi(b);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-              mma16816(acc[nb][i], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, wf[nb][kt][0],
-                       wf[nb][kt][1]);
+            for (int nb = 0; nb < NB; ++nb) mma16816(acc[nb][i], a0, a1, a2, a3, wf[nb][kt][0], wf[nb][kt][1]);
           }
         }
       }
@@ -488,7 +508,7 @@ __global__ void __launch_bounds__(L::kThreads, 1)
       if (lane == 0) mbar_arrive(&empty[slot]);
       if (un.flags & kLast) {
         // ---- the segment's sums: whole items to the output, others to their partial
-        const float un_w = 0x1p24f * pow2(e_run - 14);  // undoes the codes' 2^-24 and W's power of two
+        const float un_w = pow2(e_run - 14);  // undoes W's power of two
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -507,7 +527,7 @@ __global__ void __launch_bounds__(L::kThreads, 1)
               const float lo = kSplit ? acc[nb][i][0] + acc[nb][i][1] : acc[nb][i][j];
               const float hi = kSplit ? acc[nb][i][2] + acc[nb][i][3] : acc[nb][i][2 + j];
               o[2 * i] = fmaf(lo, un_w, z);
-              o[2 * i + 1] = fmaf(hi, un_w * 0.0625f, z);
+              o[2 * i + 1] = fmaf(hi, un_w, z);
             }
             if (un.flags & kWhole) {
               const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // no key seen: zeros; NaN stays
@@ -539,7 +559,7 @@ __global__ void __launch_bounds__(L::kThreads, 1)
     unsigned base = 0, before = 0;  // pages before the chunk, and before sequence b
     for (int c0 = 0; c0 < B_seqs; c0 += L::kThreads) {
       if (c0 > 0) {
-        const unsigned x = warp_scan(pages_of(c0 + threadIdx.x));
+        const unsigned x = warp_scan(work_of(c0 + threadIdx.x));
         __syncthreads();
         scan[threadIdx.x] = x;
         if (lane == 31) misc[16 + warp] = x;
@@ -548,7 +568,7 @@ __global__ void __launch_bounds__(L::kThreads, 1)
       const unsigned want = u0 / H;  // the page where the range begins
       for (int w = 0; w <= kWarps; ++w) {
         const unsigned in = misc[16 + w];
-        if (count > 0 && want >= base && want < base + in) {
+        if (u0 < u1 && want >= base && want < base + in) {
           int i = 0;  // the first of the warp's 32 sequences whose running sum passes it
           for (int o = 16; o; o >>= 1)
             if (scan[32 * w + i + o - 1] <= want - base) i += o;
@@ -560,21 +580,35 @@ __global__ void __launch_bounds__(L::kThreads, 1)
     }
     if (lane < kWarps) {
       int first = 0, len = 0, n = 0, q0 = 0;
-      unsigned pages = 0, h = 0, pg = 0;
-      if (count > 0) {
-        pages = seq_pages(p, b, &first, &len, &n, &q0);
-        const unsigned o = u0 - before * H;
-        h = o / pages;
-        pg = o - h * pages;
+      unsigned pages = 0;
+      auto open_seq = [&]() {  // plan of sequence b
+        if (b < L::kThreads) {
+          const int4 v = seqs[b];
+          first = v.x;
+          len = v.y;
+          n = v.z;
+          q0 = v.w;
+          pages = n > 0 ? max(1, (len + kKvPage - 1) / kKvPage - first) : 0;
+        } else {
+          pages = seq_pages(p, b, &first, &len, &n, &q0);
+        }
+      };
+      unsigned h = 0, pg = 0, item0 = 0;  // head, page of the item, and where the item's work begins
+      if (u0 < u1) {
+        open_seq();
+        const unsigned o = u0 - before * H, work = pages + kItemCost;
+        h = o / work;
+        item0 = before * H + h * work;
+        pg = u0 - item0 > kItemCost ? u0 - item0 - kItemCost : 0;
       }
       bool fresh = true;    // the segment's first page
-      unsigned seg0 = 0;    // and its place in the range
+      unsigned seg0 = 0;    // that page
       unsigned k = 0;
       int stage = 0;
       unsigned phase = 1;
       // The lanes poll without blocking, each going on as soon as its own warp has freed a slot.
       unsigned long long since = global_timer_ns();
-      while (k < count) {
+      for (bool more = true; more;) {
         const int slot = lane * kStages + stage;
         if (!mbar_test(&empty[slot], phase)) {
           if (*abort_flag) break;
@@ -586,12 +620,20 @@ __global__ void __launch_bounds__(L::kThreads, 1)
           __nanosleep(40);
           continue;
         }
+        Unit un;
+        const unsigned at = item0 + kItemCost + pg;  // the page's place in the work
+        more = at < u1;
+        if (!more) {
+          un.flags = kStop;
+          units[slot] = un;
+          mbar_arrive(&ready[slot]);
+          break;
+        }
         const int page_i = first + static_cast<int>(pg);
         int page = -1;
         if (len > 0) page = p.c.page_table[static_cast<int64_t>(b) * p.c.max_pages + page_i];
         const bool last_of_item = pg == pages - 1;
-        if (fresh) seg0 = k;
-        Unit un;
+        if (fresh) seg0 = pg;
         un.key0 = page_i * kKvPage;
         un.len = len;
         un.n = n;
@@ -603,8 +645,8 @@ __global__ void __launch_bounds__(L::kThreads, 1)
           if (len > 0) atomicOr(p.err, kErrBadIndex);
           page = -1;
         }
-        un.flags = (page >= 0 ? kValid : 0) | (fresh ? kFirst : 0) | (last_of_item || k == count - 1 ? kLast : 0) |
-                   (last_of_item && k - seg0 == pages - 1 ? kWhole : 0);
+        un.flags = (page >= 0 ? kValid : 0) | (fresh ? kFirst : 0) | (last_of_item || at + 1 == u1 ? kLast : 0) |
+                   (last_of_item && seg0 == 0 ? kWhole : 0);
         units[slot] = un;
         mbar_arrive(&ready[slot]);
         if (page >= 0) {
@@ -614,22 +656,26 @@ __global__ void __launch_bounds__(L::kThreads, 1)
         } else {
           mbar_arrive(&full[slot]);
         }
-        if (fresh && pg == 0) {  // this range holds the item's beginning: say which warp holds its end
-          const unsigned z = u0 + k + pages - 1, wide = ur * (uq + 1);
+        if (pg == 0) {  // this range holds the item's first page: say which warp holds its last one
+          const unsigned z = at + pages - 1, wide = ur * (uq + 1);
           p.ends[un.item] = make_int2(static_cast<int>(w_me),
                                       static_cast<int>(z < wide ? z / (uq + 1) : ur + (z - wide) / uq));
         }
         since = global_timer_ns();
         fresh = last_of_item;
-        if (++pg == pages && k + 1 < count) {
+        if (last_of_item) {
           pg = 0;
-          if (++h == H) {
+          item0 += pages + kItemCost;
+          if (item0 + kItemCost < u1 && ++h == H) {
             h = 0;
             do {
               ++b;
-              pages = b < B_seqs ? seq_pages(p, b, &first, &len, &n, &q0) : 1;
+              if (b < B_seqs) open_seq();
+              else pages = 1;
             } while (pages == 0);
           }
+        } else {
+          ++pg;
         }
         ++k;
         if (++stage == kStages) {
@@ -727,9 +773,9 @@ cudaError_t launch_t(DeviceContext* ctx, Problem p, int64_t rows, const void* q,
   p.max_rows = static_cast<int>(rows);
   p.rows = static_cast<int>(rows);
   const int64_t items = static_cast<int64_t>(p.c.num_seqs) * p.c.heads;
-  const int64_t most = items * p.c.max_pages;  // units at most
-  const int64_t grid = most < ctx->num_sms ? most : ctx->num_sms;
-  if (most > 0x7fffffff) {  // units are counted in 32 bits
+  const int64_t most = items * (p.c.max_pages + static_cast<int64_t>(kItemCost));  // work at most
+  const int64_t grid = items * p.c.max_pages < ctx->num_sms ? items * p.c.max_pages : ctx->num_sms;
+  if (most > 0x7fffffff) {  // work is counted in 32 bits
     *status = BITNET_ERR_UNSUPPORTED_SHAPE;
     return cudaSuccess;
   }
