@@ -19,20 +19,22 @@
 // 16-row side and the query rows as the 8-column side: a page is read once for
 // all rows of its item, and the work stays far below what feeding it costs
 // (tcgen05 would take a 128-row tile for these 8 columns).
-//   S^T[64 keys, cols] = C_k q^T:  the codes, as c - 8, are the fp16 operand: two
-//     codes at a time masked into the mantissa of 1024 (or 16 times as large, from
-//     the higher nibble) and moved to -8 .. 7 by one fma, exactly.
+//   S^T[64 keys, cols] = C_k q^T:  the 4-bit codes themselves are the operand: a
+//     code masked out of its word is the fp16 subnormal c 2^-24 (or 16 c 2^-24 from
+//     the higher nibble, met by q / 16): one AND per two codes.
 //     q . k_j = s_j (q . (c_j - 8)) + (m_j + 8 s_j) sum(q).
-//   O^T[D, cols] = C_v^T W:  W = p_j s_j as fp16, the same operand of c_j - 8, pairs
-//     of keys put side by side by a byte permute.  sum p_j (m_j + 8 s_j) is a scalar
-//     per row.  W is kept in fp16's range by a power of two of the largest s_j met.
-//     Without the -8 (subnormal fp16 codes, one AND and no fma) the two terms are
-//     large and cancel, and the tensor core truncates its running sum: 1e-4 of the
-//     result over 4096 keys, measured.
-// Queries are scaled by a power of two per row.  fp32 queries are two fp16
-// parts in neighbouring columns (hi, lo: 22 bits), as is W then; a 16-bit query
-// is one fp16 exactly, and W takes two parts whenever the columns suffice (one
-// part rounds a probability by up to 2^-11).
+//   O^T[D, cols] = C_v^T W:  W = p_j s_j, the same operand of c_j, pairs of keys put
+//     side by side by a byte permute.  sum p_j (m_j + 8 s_j) is a scalar per row.
+// The -8 is the accumulators' first value, -8 sum(q) and -8 sum(W): without it the
+// two terms are large and cancel, and the tensor core truncates its running sum
+// (1e-4 of the result over 4096 keys, measured); with it per code (an fma per two
+// codes) the instructions, not the memory, set the pace (16 x 32768 tokens: 145
+// us against 108).
+// fp32 queries, and every query where the columns suffice (at most 4 rows), are two
+// fixed-point parts in neighbouring columns: 11 + 11 bits of the row's largest
+// magnitude, as W is of the page's; every product and sum of integers is then
+// exact in fp32 (2^11 x 15 x 256 < 2^24).  More rows of 16-bit queries take one
+// fp16 each: the query exactly, a probability rounded by up to 2^-11.
 #include <type_traits>
 
 #include "common.cuh"
@@ -66,26 +68,11 @@ __device__ __forceinline__ uint32_t movm(uint32_t a) {
   return d;
 }
 
-// Codes in bits 0-3 (4-7) of both halves of w, other bits ignored, to fp16 c - 8.
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
-  const uint32_t x = (w & 0x000f000fu) | 0x64006400u;  // 1024 + c
-  const uint32_t k = 0x64086408u;                      // 1032
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&k));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
-  const uint32_t x = (w & 0x00f000f0u) | 0x64006400u;        // 1024 + 16 c
-  const uint32_t k = 0x2c002c00u, m = 0xd480d480u;           // 1/16, -72
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&k),
-                            *reinterpret_cast<const __half2*>(&m));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 __device__ __forceinline__ uint32_t pack_h2(__half a, __half b) {
   return static_cast<uint32_t>(__half_as_ushort(a)) | (static_cast<uint32_t>(__half_as_ushort(b)) << 16);
 }
 
-// 2^(14 - e) for 2^e <= v < 2^(e+1), e kept in [-100, 110]: v times it is below 2^15.
+// e of 2^e <= v < 2^(e+1), kept in [-100, 110].
 __device__ __forceinline__ int pow2_exp(float v) {
   const int e = (__float_as_int(v) >> 23) - 127;
   return min(max(e, -100), 110);
@@ -166,6 +153,8 @@ __global__ void __launch_bounds__(L::kThreads, 1)
   constexpr int kWordsK = D / 32;            // words of a key row per lane (a quarter row)
   constexpr int kTiles = D / 16;             // 16-dimension tiles of the output
   constexpr int kCols = kSplit ? 1 : 2;      // scores per key, column block and lane
+  constexpr int kExp = kSplit ? 10 : 14;     // queries and W are scaled to below 2^(kExp + 1)
+  constexpr float kLo = 0x1p-11f;            // what the low part counts
   extern __shared__ __align__(1024) uint8_t smem[];
   Unit* units = reinterpret_cast<Unit*>(smem + L::offUnit);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::offBar);  // the page's bytes have landed
@@ -246,10 +235,10 @@ __global__ void __launch_bounds__(L::kThreads, 1)
     // ------------------------------------------------------------ consumer
     const int g = lane >> 2, t = lane & 3;
     const int pg = g ^ ((g >> 1) & 1);  // key of tile row g: spreads the rows that lanes read together over the banks
-    float acc[NB][kTiles][4];
+    float acc[NB][2 * kTiles][kCols];  // o of dimension 2 kTiles g + i, in true units relative to m_run
     float m_run[NB][kCols], l_run[NB][kCols], z_run[NB][kCols], qsum[NB][kCols], qc[NB][kCols];
+    float s_init[NB][2];  // -8 sum(q) of columns 2t, 2t + 1, in the codes' 2^-24
     uint32_t qf[NB][kWordsK][4];
-    int e_run = -100;
     int stage = 0;
     unsigned phase = 0;
     for (;;) {
@@ -261,13 +250,12 @@ __global__ void __launch_bounds__(L::kThreads, 1)
       const int rows = un.n * p.G;
       if (un.flags & kFirst) {
         // ---- the item's queries as B fragments: column g, dimensions (D / 4) t ..
-        e_run = -100;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-          for (int i = 0; i < kTiles; ++i)
+          for (int i = 0; i < 2 * kTiles; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[nb][i][j] = 0.0f;
+            for (int j = 0; j < kCols; ++j) acc[nb][i][j] = 0.0f;
           const int r = nb * kRowsNb + (kSplit ? g >> 1 : g);
           const bool on = r < rows;
           const int i_tok = on ? r / p.G : 0;
@@ -287,32 +275,42 @@ __global__ void __launch_bounds__(L::kThreads, 1)
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
           const int e = pow2_exp(top);
-          const float f = pow2(14 - e);
+          const float f = pow2(kExp - e);
           float sum = 0.0f;
           __half h[D / 4];
 #pragma unroll
           for (int i = 0; i < D / 4; ++i) {
             const float x = v[i] * f;
-            h[i] = __float2half_rn(x);
-            if (kSplit && (g & 1)) h[i] = __float2half_rn(x - __half2float(h[i]));
+            if constexpr (kSplit) {
+              const float hi = rintf(x);
+              h[i] = __float2half_rn((g & 1) ? rintf((x - hi) * 0x1p11f) : hi);
+            } else {
+              h[i] = __float2half_rn(x);
+            }
             sum += __half2float(h[i]);
           }
+          const __half inv16 = __float2half_rn(0.0625f);
 #pragma unroll
           for (int w = 0; w < kWordsK; ++w) {
-            // nibbles i and i + 4 of a word come side by side
-#pragma unroll
-            for (int i = 0; i < 4; ++i) qf[nb][w][i] = pack_h2(h[8 * w + i], h[8 * w + i + 4]);
+            const __half* x = h + 8 * w;  // nibbles i and i + 4 of a word come side by side
+            qf[nb][w][0] = pack_h2(x[0], x[4]);
+            qf[nb][w][1] = pack_h2(__hmul(x[1], inv16), __hmul(x[5], inv16));
+            qf[nb][w][2] = pack_h2(x[2], x[6]);
+            qf[nb][w][3] = pack_h2(__hmul(x[3], inv16), __hmul(x[7], inv16));
           }
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
           // to the lanes that hold the scores of these columns: 2t and 2t + 1
           const float s0 = __shfl_sync(0xffffffffu, sum, 8 * t), s1 = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
           const int e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
-          qsum[nb][0] = kSplit ? s0 + s1 : s0;
-          qc[nb][0] = p.scale * pow2(e0 - 14);  // undoes the row's power of two
+          s_init[nb][0] = s0 * -0x1p-21f;
+          s_init[nb][1] = s1 * -0x1p-21f;
+          // sum(q) in the scores' units, which qc undoes: the codes' 2^-24 and the row's power of two
+          qsum[nb][0] = (kSplit ? fmaf(s1, kLo, s0) : s0) * 0x1p-24f;
+          qc[nb][0] = p.scale * pow2(e0 - kExp) * 0x1p24f;
           if constexpr (!kSplit) {
-            qsum[nb][1] = s1;
-            qc[nb][1] = p.scale * pow2(e1 - 14);
+            qsum[nb][1] = s1 * 0x1p-24f;
+            qc[nb][1] = p.scale * pow2(e1 - kExp) * 0x1p24f;
           }
 #pragma unroll
           for (int j = 0; j < kCols; ++j) {
@@ -335,7 +333,7 @@ __global__ void __launch_bounds__(L::kThreads, 1)
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sc[nb][kt][j] = 0.0f;
+            for (int j = 0; j < 4; ++j) sc[nb][kt][j] = s_init[nb][j & 1];
           const uint4* r0 = reinterpret_cast<const uint4*>(blk + B::offK + (16 * kt + pg) * B::kRow + (B::kRow / 4) * t);
           const uint4* r1 = reinterpret_cast<const uint4*>(blk + B::offK + (16 * kt + pg + 8) * B::kRow + (B::kRow / 4) * t);
 #pragma unroll
@@ -345,13 +343,12 @@ __global__ void __launch_bounds__(L::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t ah = wa[i] >> 8, bh = wb[i] >> 8;
-              const uint32_t a0 = codes_lo(wa[i]), a1 = codes_lo(wb[i]), a2 = codes_hi(wa[i]), a3 = codes_hi(wb[i]);
-              const uint32_t c0 = codes_lo(ah), c1 = codes_lo(bh), c2 = codes_hi(ah), c3 = codes_hi(bh);
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
                 const uint32_t* f = qf[nb][4 * c + i];
-                mma16816(sc[nb][kt], a0, a1, a2, a3, f[0], f[1]);
-                mma16816(sc[nb][kt], c0, c1, c2, c3, f[2], f[3]);
+                mma16816(sc[nb][kt], wa[i] & 0x000f000fu, wb[i] & 0x000f000fu, wa[i] & 0x00f000f0u, wb[i] & 0x00f000f0u,
+                         f[0], f[1]);
+                mma16816(sc[nb][kt], ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u, bh & 0x00f000f0u, f[2], f[3]);
               }
             }
           }
@@ -360,14 +357,10 @@ __global__ void __launch_bounds__(L::kThreads, 1)
         const int pos0 = un.len - un.n;  // position of the item's first query token
         const bool inner = un.key0 + kKvPage <= (p.causal ? pos0 + 1 : un.len) &&
                            (!p.causal || p.window == 0 || un.key0 > un.len - 1 - p.window);
-        float x[NB][8][kCols], mx[NB][kCols];
+        float x[NB][8][kCols];
         float vs[8], vm[8], smax = 0.0f;
         const float2* kmeta = reinterpret_cast<const float2*>(blk + B::offKMeta);
         const float2* vmeta = reinterpret_cast<const float2*>(blk + B::offVMeta);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int j = 0; j < kCols; ++j) mx[nb][j] = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int key = 16 * (i >> 1) + 8 * (i & 1) + pg;
@@ -382,7 +375,7 @@ __global__ void __launch_bounds__(L::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < kCols; ++j) {
               const float* s4 = sc[nb][i >> 1] + 2 * (i & 1);
-              const float dot = kSplit ? s4[0] + s4[1] : s4[j];
+              const float dot = kSplit ? fmaf(s4[1], kLo, s4[0]) : s4[j];
               x[nb][i][j] = fmaf(dot, km.x, kmid * qsum[nb][j]) * qc[nb][j];
             }
           }
@@ -406,10 +399,14 @@ __global__ void __launch_bounds__(L::kThreads, 1)
         smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 4));
         smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 8));
         smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 16));
-        const int e_new = max(e_run, pow2_exp(smax));
-        bool moved = e_new != e_run;
+        const int e_pg = pow2_exp(smax);  // the page's W = p s 2^(kExp - e_pg), p relative to its own maximum
+        const float vf = pow2(kExp - e_pg);
+        uint32_t wf[NB][4][2];
+        float w_init[NB][2];              // -8 sum(W) of columns 2t, 2t + 1, in the codes' 2^-24
+        float fa[NB][kCols], fb[NB][kCols];  // what the running sums and the page's count for from now on
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb) {
+          float wsum[2] = {0.0f, 0.0f}, lp[kCols], zp[kCols], mref[kCols];
 #pragma unroll
           for (int j = 0; j < kCols; ++j) {
             float v = x[nb][0][j];
@@ -418,89 +415,98 @@ __global__ void __launch_bounds__(L::kThreads, 1)
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            mx[nb][j] = fmaxf(m_run[nb][j], v);
-            moved |= mx[nb][j] != m_run[nb][j];
+            mref[j] = v == -INFINITY ? 0.0f : v;  // no key: -inf - -inf must not reach the exponential
+            const float m_new = fmaxf(m_run[nb][j], v);
+            const float ref = m_new == -INFINITY ? 0.0f : m_new;
+            fa[nb][j] = ex2(m_run[nb][j] - ref);
+            fb[nb][j] = ex2(v - ref);
+            m_run[nb][j] = m_new;
+            lp[j] = 0.0f;
+            zp[j] = 0.0f;
           }
-        if (__any_sync(0xffffffffu, moved)) {
-          const float fe = e_new == e_run ? 1.0f : ex2(static_cast<float>(e_run - e_new));
-          e_run = e_new;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            float a[2];
-#pragma unroll
-            for (int j = 0; j < kCols; ++j) {
-              // nothing seen so far: every sum is 0, and -inf - -inf must not reach the exponential
-              const float al = m_run[nb][j] == -INFINITY ? 0.0f : ex2(m_run[nb][j] - mx[nb][j]);
-              m_run[nb][j] = mx[nb][j];
-              l_run[nb][j] *= al;
-              z_run[nb][j] *= al;
-              a[j] = al * fe;
-            }
-            if constexpr (kSplit) a[1] = a[0];
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-              acc[nb][i][0] *= a[0];
-              acc[nb][i][1] *= a[1];
-              acc[nb][i][2] *= a[0];
-              acc[nb][i][3] *= a[1];
-            }
-          }
-        }
-        // ---- probabilities, their sums, and W as B fragments
-        const float vf = pow2(14 - e_run);
-        uint32_t wf[NB][4][2];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          float mref[kCols];
-#pragma unroll
-          for (int j = 0; j < kCols; ++j) mref[j] = m_run[nb][j] == -INFINITY ? 0.0f : m_run[nb][j];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            __half hw[2];
+            float part[2];
 #pragma unroll
             for (int j = 0; j < kCols; ++j) {
               const bool none = !inner && x[nb][i][j] == -INFINITY;  // masked: whatever its value row holds
               const float pr = ex2(x[nb][i][j] - mref[j]);
               const float w = none ? 0.0f : pr * (vs[i] * vf);
-              l_run[nb][j] += pr;
-              hw[j] = __float2half_rn(w);
-              if constexpr (kSplit) hw[1] = __float2half_rn(w - __half2float(hw[0]));
-              z_run[nb][j] += none ? 0.0f : pr * vm[i];
+              lp[j] += pr;
+              zp[j] += none ? 0.0f : pr * vm[i];
+              if constexpr (kSplit) {
+                part[0] = rintf(w);
+                part[1] = rintf((w - part[0]) * 0x1p11f);
+              } else {
+                part[j] = __half2float(__float2half_rn(w));
+              }
             }
-            wf[nb][i >> 1][i & 1] = movm(pack_h2(hw[0], hw[1]));
+            wsum[0] += part[0];
+            wsum[1] += part[1];
+            wf[nb][i >> 1][i & 1] = movm(pack_h2(__float2half_rn(part[0]), __float2half_rn(part[1])));
+          }
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            l_run[nb][j] = fmaf(l_run[nb][j], fa[nb][j], lp[j] * fb[nb][j]);
+            z_run[nb][j] = fmaf(z_run[nb][j], fa[nb][j], zp[j] * fb[nb][j]);
+            fb[nb][j] *= pow2(e_pg - kExp) * 0x1p24f;
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float v = wsum[j];
+            v += __shfl_xor_sync(0xffffffffu, v, 4);
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            v += __shfl_xor_sync(0xffffffffu, v, 16);
+            w_init[nb][j] = v * -0x1p-21f;
           }
         }
-        // ---- O^T += C_v^T W: keys 2t, 2t + 1 (and 8 on) of tile kt, this lane's 2 kTiles dimensions of each
+        // ---- O^T of the page = C_v^T W, a 16-dimension tile at a time: bytes i of a lane's part of the value rows,
+        // keys 2t, 2t + 1 (and 8 on) of the four key tiles
         const int k0 = (2 * t) ^ (t & 1), k1 = (2 * t + 1) ^ (t & 1);  // keys of tile rows 2t, 2t + 1
         constexpr int kVw = D / 64;  // words of a value row per lane
+        const uint8_t* v0 = blk + B::offV + k0 * B::kRow + 4 * kVw * g;
+        const uint8_t* v1 = blk + B::offV + k1 * B::kRow + 4 * kVw * g;
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-          uint32_t w[4][kVw];
+        for (int wi = 0; wi < kVw; ++wi) {
+          uint32_t w[4][4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int key = 16 * kt + 8 * (r >> 1) + ((r & 1) ? k1 : k0);
-            const uint8_t* src = blk + B::offV + key * B::kRow + 4 * kVw * g;
-            if constexpr (kVw == 2) {
-              const uint2 v = *reinterpret_cast<const uint2*>(src);
-              w[r][0] = v.x;
-              w[r][1] = v.y;
-            } else {
-              const uint4 v = *reinterpret_cast<const uint4*>(src);
-              w[r][0] = v.x;
-              w[r][1] = v.y;
-              w[r][2] = v.z;
-              w[r][3] = v.w;
-            }
+          for (int kt = 0; kt < 4; ++kt) {
+            w[kt][0] = *reinterpret_cast<const uint32_t*>(v0 + 16 * kt * B::kRow + 4 * wi);
+            w[kt][1] = *reinterpret_cast<const uint32_t*>(v1 + 16 * kt * B::kRow + 4 * wi);
+            w[kt][2] = *reinterpret_cast<const uint32_t*>(v0 + (16 * kt + 8) * B::kRow + 4 * wi);
+            w[kt][3] = *reinterpret_cast<const uint32_t*>(v1 + (16 * kt + 8) * B::kRow + 4 * wi);
           }
 #pragma unroll
-          for (int i = 0; i < kTiles; ++i) {
-            // byte i of both keys in the two halves: low nibbles dimension 2i, high nibbles 2i + 1
-            const uint32_t sel = (i & 3) | ((4 + (i & 3)) << 8);
-            const uint32_t a = prmt_b32(w[0][i >> 2], w[1][i >> 2], sel);
-            const uint32_t b = prmt_b32(w[2][i >> 2], w[3][i >> 2], sel);
-            const uint32_t a0 = codes_lo(a), a1 = codes_hi(a), a2 = codes_lo(b), a3 = codes_hi(b);
+          for (int bi = 0; bi < 4; ++bi) {
+            const int i = 4 * wi + bi;
+            float pg_o[NB][4];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816(acc[nb][i], a0, a1, a2, a3, wf[nb][kt][0], wf[nb][kt][1]);
+            for (int nb = 0; nb < NB; ++nb) {
+              pg_o[nb][0] = w_init[nb][0];
+              pg_o[nb][1] = w_init[nb][1];
+              pg_o[nb][2] = 16.0f * w_init[nb][0];
+              pg_o[nb][3] = 16.0f * w_init[nb][1];
+            }
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt) {
+              // byte bi of both keys in the two halves: low nibbles dimension 2i, high nibbles 2i + 1
+              const uint32_t sel = bi | ((4 + bi) << 8);
+              const uint32_t a = prmt_b32(w[kt][0], w[kt][1], sel);
+              const uint32_t b = prmt_b32(w[kt][2], w[kt][3], sel);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma16816(pg_o[nb], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, wf[nb][kt][0],
+                         wf[nb][kt][1]);
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int j = 0; j < kCols; ++j) {
+                const float lo = kSplit ? fmaf(pg_o[nb][1], kLo, pg_o[nb][0]) : pg_o[nb][j];
+                const float hi = kSplit ? fmaf(pg_o[nb][3], kLo, pg_o[nb][2]) : pg_o[nb][2 + j];
+                acc[nb][2 * i][j] = fmaf(lo, fb[nb][j], acc[nb][2 * i][j] * fa[nb][j]);
+                acc[nb][2 * i + 1][j] = fmaf(hi, fb[nb][j] * 0.0625f, acc[nb][2 * i + 1][j] * fa[nb][j]);
+              }
           }
         }
       }
@@ -508,7 +514,6 @@ __global__ void __launch_bounds__(L::kThreads, 1)
       if (lane == 0) mbar_arrive(&empty[slot]);
       if (un.flags & kLast) {
         // ---- the segment's sums: whole items to the output, others to their partial
-        const float un_w = pow2(e_run - 14);  // undoes W's power of two
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -523,12 +528,7 @@ __global__ void __launch_bounds__(L::kThreads, 1)
             if (r >= rows) continue;
             float o[2 * kTiles];
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-              const float lo = kSplit ? acc[nb][i][0] + acc[nb][i][1] : acc[nb][i][j];
-              const float hi = kSplit ? acc[nb][i][2] + acc[nb][i][3] : acc[nb][i][2 + j];
-              o[2 * i] = fmaf(lo, un_w, z);
-              o[2 * i + 1] = fmaf(hi, un_w, z);
-            }
+            for (int i = 0; i < 2 * kTiles; ++i) o[i] = acc[nb][i][j] + z;
             if (un.flags & kWhole) {
               const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // no key seen: zeros; NaN stays
               const int i_tok = r / p.G;
