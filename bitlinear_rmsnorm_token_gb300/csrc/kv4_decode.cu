@@ -107,8 +107,10 @@ struct Layout {
   static constexpr int offUnit = kSlots * KvBlock<D>::kBytes;
   static constexpr int offBar = offUnit + kSlots * static_cast<int>(sizeof(Unit));
   static constexpr int offScan = offBar + 3 * kSlots * 8;
-  static constexpr int offSeq = (offScan + kThreads * 4 + 15) / 16 * 16;  // plan of the first kThreads sequences
-  static constexpr int offMisc = offSeq + kThreads * 16;  // per-warp sums (two sets), abort flag
+  static constexpr int kPer = (512 + kThreads - 1) / kThreads;  // sequences per thread of a running sum
+  static constexpr int kSeqs = kPer * kThreads;
+  static constexpr int offSeq = (offScan + kThreads * 4 + 15) / 16 * 16;  // plan of the first kSeqs sequences
+  static constexpr int offMisc = offSeq + kSeqs * 16;  // per-warp sums (two sets), abort flag
   static constexpr int kBytes = offMisc + 256;
   static_assert(kBytes <= 232448, "over the 227 KB of shared memory a CTA may use");
 };
@@ -169,19 +171,28 @@ __global__ void __launch_bounds__(L::kThreads, 1)
   const unsigned H = p.c.heads;
   pdl_launch_dependents();
   // ---- total work (it fits 32 bits, checked on the host), then each producer lane finds where its warp's range
-  // begins: a running sum over the sequences, kThreads of them at a time
+  // begins: a running sum over the sequences, kSeqs of them at a time, kPer neighbours to a thread
   int4* seqs = reinterpret_cast<int4*>(smem + L::offSeq);  // first page, length, rows, first row
+  auto work_of_pages = [](unsigned pages) { return pages ? pages + kItemCost : 0; };
   auto work_of = [&](int b) -> unsigned {
     int f, l, n, q0;
-    const unsigned pages = b < B_seqs ? seq_pages(p, b, &f, &l, &n, &q0) : 0;
-    return pages ? pages + kItemCost : 0;
+    return b < B_seqs ? work_of_pages(seq_pages(p, b, &f, &l, &n, &q0)) : 0;
+  };
+  auto chunk_work = [&](int c0) {  // of this thread's sequences of the chunk
+    unsigned sum = 0;
+#pragma unroll
+    for (int j = 0; j < L::kPer; ++j) sum += work_of(c0 + L::kPer * static_cast<int>(threadIdx.x) + j);
+    return sum;
   };
   unsigned work0 = 0;
-  if (static_cast<int>(threadIdx.x) < B_seqs) {
-    int4 v = make_int4(0, 0, 0, 0);
-    work0 = seq_pages(p, threadIdx.x, &v.x, &v.y, &v.z, &v.w);
-    if (work0) work0 += kItemCost;
-    seqs[threadIdx.x] = v;
+#pragma unroll
+  for (int j = 0; j < L::kPer; ++j) {
+    const int b = L::kPer * static_cast<int>(threadIdx.x) + j;
+    if (b < B_seqs) {
+      int4 v = make_int4(0, 0, 0, 0);
+      work0 += work_of_pages(seq_pages(p, b, &v.x, &v.y, &v.z, &v.w));
+      seqs[b] = v;
+    }
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kSlots; ++i) {
@@ -201,7 +212,7 @@ __global__ void __launch_bounds__(L::kThreads, 1)
     return x;
   };
   unsigned mine = work0;
-  for (int b = threadIdx.x + L::kThreads; b < B_seqs; b += L::kThreads) mine += work_of(b);
+  for (int c0 = L::kSeqs; c0 < B_seqs; c0 += L::kSeqs) mine += chunk_work(c0);
   const unsigned sum = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0) misc[warp] = sum;
   {
@@ -225,8 +236,8 @@ __global__ void __launch_bounds__(L::kThreads, 1)
 
   if (warp < kWarps) {
     // further sequences: the producer searches, the consumers take part in the running sums
-    for (int c0 = L::kThreads; c0 < B_seqs; c0 += L::kThreads) {
-      const unsigned x = warp_scan(work_of(c0 + threadIdx.x));
+    for (int c0 = L::kSeqs; c0 < B_seqs; c0 += L::kSeqs) {
+      const unsigned x = warp_scan(chunk_work(c0));
       __syncthreads();
       scan[threadIdx.x] = x;
       if (lane == 31) misc[16 + warp] = x;
@@ -557,9 +568,18 @@ __global__ void __launch_bounds__(L::kThreads, 1)
     // ------------------------------------------------------------ producer
     int b = 0;
     unsigned base = 0, before = 0;  // pages before the chunk, and before sequence b
-    for (int c0 = 0; c0 < B_seqs; c0 += L::kThreads) {
+    auto seq_of = [&](int i) {  // plan of sequence i: from shared memory where it is there
+      if (i < L::kSeqs) return seqs[i];
+      int4 v = make_int4(0, 0, 0, 0);
+      seq_pages(p, i, &v.x, &v.y, &v.z, &v.w);
+      return v;
+    };
+    auto pages_in = [](const int4& v) {
+      return v.z > 0 ? static_cast<unsigned>(max(1, (v.y + kKvPage - 1) / kKvPage - v.x)) : 0u;
+    };
+    for (int c0 = 0; c0 < B_seqs; c0 += L::kSeqs) {
       if (c0 > 0) {
-        const unsigned x = warp_scan(work_of(c0 + threadIdx.x));
+        const unsigned x = warp_scan(chunk_work(c0));
         __syncthreads();
         scan[threadIdx.x] = x;
         if (lane == 31) misc[16 + warp] = x;
@@ -569,11 +589,19 @@ __global__ void __launch_bounds__(L::kThreads, 1)
       for (int w = 0; w <= kWarps; ++w) {
         const unsigned in = misc[16 + w];
         if (u0 < u1 && want >= base && want < base + in) {
-          int i = 0;  // the first of the warp's 32 sequences whose running sum passes it
+          int i = 0;  // the first of the warp's 32 threads whose running sum passes it, then its sequence
           for (int o = 16; o; o >>= 1)
             if (scan[32 * w + i + o - 1] <= want - base) i += o;
-          b = c0 + 32 * w + i;
+          b = c0 + L::kPer * (32 * w + i);
           before = base + (i ? scan[32 * w + i - 1] : 0);
+#pragma unroll
+          for (int j = 1; j < L::kPer; ++j) {
+            const unsigned in_b = b < B_seqs ? work_of_pages(pages_in(seq_of(b))) : 0;
+            if (want >= before + in_b) {
+              before += in_b;
+              ++b;
+            }
+          }
         }
         base += in;
       }
@@ -582,16 +610,12 @@ __global__ void __launch_bounds__(L::kThreads, 1)
       int first = 0, len = 0, n = 0, q0 = 0;
       unsigned pages = 0;
       auto open_seq = [&]() {  // plan of sequence b
-        if (b < L::kThreads) {
-          const int4 v = seqs[b];
-          first = v.x;
-          len = v.y;
-          n = v.z;
-          q0 = v.w;
-          pages = n > 0 ? max(1, (len + kKvPage - 1) / kKvPage - first) : 0;
-        } else {
-          pages = seq_pages(p, b, &first, &len, &n, &q0);
-        }
+        const int4 v = seq_of(b);
+        first = v.x;
+        len = v.y;
+        n = v.z;
+        q0 = v.w;
+        pages = pages_in(v);
       };
       unsigned h = 0, pg = 0, item0 = 0;  // head, page of the item, and where the item's work begins
       if (u0 < u1) {
@@ -761,10 +785,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv4_join(const Problem p, O
 }
 
 // Warps and ring slots: as many page blocks as shared memory holds, and the
-// registers of the variant (9 warps: 168 a thread, 8 or 7: 255).
+// registers of the variant (up to 12 warps with the producer: 168 a thread, up
+// to 8: 255).  16 x 32768 tokens of bf16 with 8 x 3, 8 x 2, 12 x 2 and 11 x 2
+// consumer warps x slots: 118, 117, 112 and 111 us.
 template <int D, int NB>
 using LayoutOf =
-    std::conditional_t<D == 128, std::conditional_t<NB == 1, Layout<128, 8, 3>, Layout<128, 7, 3>>, Layout<256, 6, 2>>;
+    std::conditional_t<D == 128, std::conditional_t<NB == 1, Layout<128, 11, 2>, Layout<128, 7, 3>>, Layout<256, 6, 2>>;
 
 template <int D, int NB, bool kSplit, typename QT, typename OT>
 cudaError_t launch_t(DeviceContext* ctx, Problem p, int64_t rows, const void* q, void* out, cudaStream_t s,

@@ -529,3 +529,16 @@ def test_decoder_layer_run(device):
         yw = bn.bitlinear_forward(want.float().view(T, Hq * D).contiguous(), go, *wo, K)
         # a code of the output projection's int8 input may flip where o differs in its last bits: 2e-3 of the row
         assert ((y - yw).norm(dim=1) / yw.norm(dim=1)).max() < 2e-3
+
+
+@gpu
+@pytest.mark.parametrize("B,D", [(700, 128), (1300, 256)])
+def test_many_sequences(device, B, D):
+    """More sequences than one running sum of the work division takes, empty ones among them, against one call each."""
+    r = np.random.default_rng(70)
+    lens = r.integers(0, 200, B)
+    counts = np.minimum(r.integers(0, 3, B), lens)
+    counts[5], lens[5] = 1, 0
+    c = ref.Case(71, counts.tolist(), lens.tolist(), 1, D)
+    check(c, queries(72, c.T, 2, D, F32), 2)
+    check(c, queries(72, c.T, 2, D, BF16), 2, window=70)
