@@ -1,0 +1,780 @@
+// kv4_prefill.cu -- attention of many query rows per sequence over the paged
+// 4-bit cache (prompts, chunks of prompts, whole texts) on the 5th-generation
+// tensor cores.
+//
+// A tile is 128 query rows of a (sequence, kv head): row r is query head
+// h G + r % G of token r / G, so the heads that share keys share the tile.  A CTA
+// takes two tiles (head_dim 128) or one (256) and walks the pages that their rows
+// see, 64 keys at a time, with the running maximum and sum of a one-pass softmax:
+//   S[128, 64]  = Q C_k^T   (tcgen05, fp16 operands, both in shared memory)
+//   x = s_j S + (m_j + 8 s_j) sum(q), p = 2^(c x - ref)
+//   O[128, D] += W C_v      (W = p s_j as fp16 from tensor memory)
+// with C the cache's codes as c - 8 in fp16, exact; the scales stay out of the
+// products (kv4.cuh).  O, S and W live in tensor memory; W takes S's place.
+// A row's reference only moves when its maximum has grown by 2^8 (O is then
+// rescaled); W is kept in fp16's range by a power of two of the largest value
+// scale met, which moves in the same way.  fp32 queries and their W are two fp16
+// parts each (22 bits), two products where 16-bit ones take one.
+//
+// Warps: 4 per tile for the softmax (a thread a row), 4 that decode pages into
+// the operands' swizzled layout (values transposed: rows are dimensions, in the
+// order that keeps the stores of a warp on different banks), a producer of raw
+// pages, and an MMA issuer per tile.  S is double buffered, so that the next
+// page's scores are computed while a page's softmax runs.
+// Few tiles on a long cache: the pages are split over gridDim.z and the parts
+// joined by a second launch, in order.
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+#include "rowquant.cuh"
+
+namespace bitnet {
+namespace {
+
+constexpr int kRows = 128;          // rows of a tile
+constexpr int kUnpackWarps = 4;
+constexpr float kLazy = 8.0f;       // a row's maximum may pass its reference by this many powers of two
+constexpr int kWExp = 6;            // value scales are below 2^(kWExp + 1) after their power of two: times 2^kLazy < 2^15
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
+// e of 2^e <= v < 2^(e+1), kept in [-100, 100].
+__device__ __forceinline__ int pow2_exp(float v) { return min(max((__float_as_int(v) >> 23) - 127, -100), 100); }
+
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Codes in bits 0-3 (4-7) of both halves of w, other bits ignored, to fp16 c - 8.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
+  const uint32_t x = (w & 0x000f000fu) | 0x64006400u;  // 1024 + c
+  const uint32_t k = 0x64086408u;                      // 1032
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
+  const uint32_t x = (w & 0x00f000f0u) | 0x64006400u;    // 1024 + 16 c
+  const uint32_t k = 0x2c002c00u, m = 0xd480d480u;       // 1/16, -72
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&k),
+                            *reinterpret_cast<const __half2*>(&m));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, fp16 operands: A's column c holds K elements 2c, 2c + 1.
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x4(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr)
+               : "memory");
+}
+
+// A page's per-key factors, and what the softmax has to know of the page.
+struct __align__(16) PageMeta {
+  float2 k[kKvPage];  // s, m + 8 s of the keys
+  float2 v[kKvPage];  // s 2^(kWExp - e), m + 8 s of the values
+  int key0;           // position of the page's first token
+  int ok;             // 0: no such page, its keys are masked
+  int grow;           // e has grown by this much since the page before
+  int e;
+};
+
+template <int D, bool kSplit>
+struct Layout {
+  static constexpr int kT = D == 128 ? 2 : 1;                // tiles per CTA
+  static constexpr int kParts = kSplit ? 2 : 1;
+  static constexpr int kRaw = D == 256 && kSplit ? 1 : 2;    // raw page slots
+  static constexpr int kK = D == 256 && kSplit ? 1 : 2;      // key operand stages
+  static constexpr int kV = D == 256 ? 1 : 2;                // value operand stages
+  static constexpr int kMeta = 4;
+  static constexpr int kSoftWarps = 4 * kT;
+  static constexpr int kProducer = kSoftWarps + kUnpackWarps;
+  static constexpr int kMma0 = kProducer + 1;
+  static constexpr int kThreads = 32 * (kMma0 + kT);
+  static constexpr int kQPart = kRows * D * 2;               // bytes of one part of a tile's queries
+  static constexpr int kOp = kKvPage * D * 2;                // bytes of a page's keys (values) as fp16
+  static constexpr int offQ = 0;
+  static constexpr int offK = offQ + kT * kParts * kQPart;
+  static constexpr int offV = offK + kK * kOp;
+  static constexpr int offRaw = offV + kV * kOp;
+  static constexpr int offMeta = offRaw + kRaw * KvBlock<D>::kBytes;
+  static constexpr int kNumBars = 2 * kRaw + 2 * kK + 2 * kV + 2 * kMeta + 5 * kT;
+  static constexpr int offBar = offMeta + kMeta * static_cast<int>(sizeof(PageMeta));
+  static constexpr int offMisc = offBar + kNumBars * 8;      // 32 ints
+  static constexpr int kBytes = offMisc + 128;
+  static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 232448, "over the 227 KB of shared memory a CTA may use");
+  // tensor memory: scores (two buffers) and output of each tile
+  static constexpr int kCols = 512;
+  __host__ __device__ static constexpr int s_col(int t, int buf) { return D == 128 ? 256 * t + 64 * buf : 256 + 64 * buf; }
+  __host__ __device__ static constexpr int o_col(int t) { return D == 128 ? 256 * t + 128 : 0; }
+};
+
+struct Problem {
+  KvView c;
+  int Hq, G, T, max_q;
+  float scale;  // |softmax scale| * log2(e)
+  float sign;   // its sign, given to the queries
+  int causal, window;
+  unsigned* err;
+  float* part;  // [splits][T * Hq][D + 4], or null
+};
+
+template <int D, bool kSplit, typename QT, typename OT>
+__global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
+    k_kv4_prefill(const Problem p, const QT* __restrict__ q, OT* __restrict__ out) {
+  using L = Layout<D, kSplit>;
+  using B = KvBlock<D>;
+  constexpr int kT = L::kT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+  PageMeta* metas = reinterpret_cast<PageMeta*>(smem + L::offMeta);
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L::offBar);
+  uint64_t* raw_empty = raw_full + L::kRaw;
+  uint64_t* k_full = raw_empty + L::kRaw;
+  uint64_t* k_empty = k_full + L::kK;
+  uint64_t* v_full = k_empty + L::kK;
+  uint64_t* v_empty = v_full + L::kV;
+  uint64_t* meta_full = v_empty + L::kV;
+  uint64_t* meta_empty = meta_full + L::kMeta;
+  uint64_t* s_full = meta_empty + L::kMeta;  // [tile][buffer]
+  uint64_t* p_full = s_full + 2 * kT;        // [tile]
+  uint64_t* pv_done = p_full + kT;           // [tile]
+  uint64_t* drained = pv_done + kT;          // [tile]: only on giving up
+  int* misc = reinterpret_cast<int*>(smem + L::offMisc);
+  volatile int* abort_flag = misc;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
+  // misc[2], misc[3]: sequence and pair of tiles; misc[8..]: running sums
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  pdl_launch_dependents();
+  // ---- which rows: unit `want` of kv head `head`, the last units (longest rows of a causal prompt) first
+  const int head = blockIdx.x % p.c.heads;
+  const int want = gridDim.x / p.c.heads - 1 - blockIdx.x / p.c.heads;
+  if (threadIdx.x == 0) misc[2] = -1;
+  {
+    int base = 0;
+    for (int c0 = 0; c0 < p.c.num_seqs; c0 += L::kThreads) {
+      const int b = c0 + threadIdx.x;
+      int units = 0;
+      if (b < p.c.num_seqs) {
+        const int q0 = p.c.q_start[b];
+        const int64_t n = static_cast<int64_t>(p.c.q_start[b + 1]) - q0;
+        if (n < 0 || n > p.max_q || q0 < 0 || q0 + n > p.T) atomicOr(p.err, kErrBadIndex);
+        else units = static_cast<int>((n * p.G + kT * kRows - 1) / (kT * kRows));
+      }
+      int x = units;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) misc[8 + warp] = x;
+      __syncthreads();
+      int before = base;
+      for (int w = 0; w < L::kThreads / 32; ++w) {
+        if (w < warp) before += misc[8 + w];
+        base += misc[8 + w];
+      }
+      const int lo = before + x - units;
+      if (want >= lo && want < lo + units) {
+        misc[2] = b;
+        misc[3] = want - lo;
+      }
+    }
+  }
+  __syncthreads();
+  const int b = misc[2];
+  if (b < 0) return;  // the grid is sized for any division of the rows
+  bool bad = false;
+  const int len = kv_len_of(p.c, b, &bad);
+  if (bad && threadIdx.x == 0) atomicOr(p.err, kErrBadIndex);
+  const int q0 = p.c.q_start[b], n = p.c.q_start[b + 1] - q0;
+  const int row0 = misc[3] * kT * kRows;              // first row of the CTA
+  const int rows = n * p.G;
+  const int pos0 = len - n;                           // position of the sequence's first query token
+  // pages that any of the CTA's rows sees
+  int page0 = 0, pages = (len + kKvPage - 1) / kKvPage;
+  if (p.causal) {
+    const int last = pos0 + (min(row0 + kT * kRows, rows) - 1) / p.G;  // position of the last row
+    pages = last < 0 ? 0 : min(pages, last / kKvPage + 1);
+    if (p.window > 0) page0 = max(0, pos0 + row0 / p.G - p.window + 1) / kKvPage;
+  }
+  {
+    const int all = max(0, pages - page0);
+    const int z = blockIdx.z, Z = gridDim.z;
+    const int a = static_cast<int>(static_cast<int64_t>(all) * z / Z);
+    pages = static_cast<int>(static_cast<int64_t>(all) * (z + 1) / Z) - a;
+    page0 += a;
+  }
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kRaw; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], kUnpackWarps);
+    }
+    for (int i = 0; i < L::kK; ++i) {
+      mbar_init(&k_full[i], kUnpackWarps);
+      mbar_init(&k_empty[i], kT);
+    }
+    for (int i = 0; i < L::kV; ++i) {
+      mbar_init(&v_full[i], kUnpackWarps);
+      mbar_init(&v_empty[i], kT);
+    }
+    for (int i = 0; i < L::kMeta; ++i) {
+      mbar_init(&meta_full[i], kUnpackWarps);
+      mbar_init(&meta_empty[i], L::kSoftWarps);
+    }
+    for (int i = 0; i < kT; ++i) {
+      mbar_init(&s_full[2 * i], 1);
+      mbar_init(&s_full[2 * i + 1], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&drained[i], 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == L::kMma0) {
+    tmem_alloc(tmem_slot, L::kCols);
+    tmem_relinquish();
+  }
+  // ---- queries: a softmax thread's row, scaled by a power of two, as fp16 (one part or two)
+  float qsum = 0.0f, qc = 0.0f;
+  const int tile = warp >> 2;                               // softmax warps
+  const int r = row0 + tile * kRows + (threadIdx.x & 127);  // row of the item
+  const bool row_on = warp < L::kSoftWarps && r < rows;
+  const int i_tok = row_on ? r / p.G : 0;
+  const int64_t q_at = (static_cast<int64_t>(q0 + i_tok) * p.Hq + head * p.G + (row_on ? r - i_tok * p.G : 0));
+  if (warp < L::kSoftWarps) {
+    const QT* src = q + q_at * D;
+    float top = 0.0f;
+    if (row_on) {
+#pragma unroll 8
+      for (int i = 0; i < D / 4; ++i) {
+        const float4 v = load4(src + 4 * i);
+        top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+      }
+    }
+    const int e = pow2_exp(top);
+    const float f = p.sign * pow2(14 - e);
+    qc = p.scale * pow2(e - 14);
+    const int rr = threadIdx.x & 127;
+#pragma unroll 2
+    for (int c = 0; c < D / 8; ++c) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 u = row_on ? load4(src + 8 * c + 4 * i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        v[4 * i] = u.x * f;
+        v[4 * i + 1] = u.y * f;
+        v[4 * i + 2] = u.z * f;
+        v[4 * i + 3] = u.w * f;
+      }
+      // chunk c of the row: dimensions 8c + 0, 4, 1, 5, 2, 6, 3, 7, the order in which a word of codes decodes
+      uint8_t* dst = smem + L::offQ + tile * L::kParts * L::kQPart + (c >> 3) * (kRows * 128) + (rr >> 3) * 1024 +
+                     (rr & 7) * 128 + (((c & 7) ^ (rr & 7)) << 4);
+      float h[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[i] = __half2float(__float2half_rn(v[i]));
+        qsum += h[i];
+      }
+      *reinterpret_cast<uint4*>(dst) =
+          make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
+      if constexpr (kSplit) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          h[i] = __half2float(__float2half_rn(v[i] - h[i]));
+          qsum += h[i];
+        }
+        *reinterpret_cast<uint4*>(dst + L::kQPart) =
+            make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
+      }
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < L::kSoftWarps) {
+    // ------------------------------------------------------------ softmax
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;  // this warp's quarter of the TMEM lanes
+    const int pos = row_on ? pos0 + i_tok : len - 1;
+    const int key_hi = p.causal ? min(pos, len - 1) : len - 1;
+    const int key_lo = p.causal && p.window > 0 ? pos - p.window + 1 : 0;
+    // pages between these need no mask for any row of the tile
+    const int tile_r0 = row0 + tile * kRows;
+    const int free_hi = p.causal ? min(pos0 + tile_r0 / p.G, len - 1) : len - 1;
+    const int free_lo = p.causal && p.window > 0 ? pos0 + (min(tile_r0 + kRows, rows) - 1) / p.G - p.window + 1 : 0;
+    float m_ref = -INFINITY, l = 0.0f, z = 0.0f;
+    int e_run = 0;
+    bool ok = true;
+    for (int j = 0; j < pages; ++j) {
+      const int buf = j & 1, ms = j % L::kMeta;
+      const uint32_t s_addr = tmem + lanes + static_cast<uint32_t>(L::s_col(tile, buf));
+      if (!mbar_wait(&meta_full[ms], (j / L::kMeta) & 1, p.err, abort_flag) ||
+          !mbar_wait(&s_full[2 * tile + buf], (j >> 1) & 1, p.err, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const PageMeta& meta = metas[ms];
+      const int key0 = meta.key0, grow = meta.grow;
+      const bool masked = !meta.ok || key0 < free_lo || key0 + kKvPage - 1 > free_hi;
+      e_run = meta.e;
+      uint32_t s0[32], s1[32];
+      tmem_ld_32x32b_x32(s_addr, s0);
+      tmem_ld_32x32b_x32(s_addr + 32, s1);
+      tmem_ld_wait();
+      tmem_reg_fence(s0);
+      tmem_reg_fence(s1);
+      float x[64];
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 64; i += 2) {
+        const float4 km = *reinterpret_cast<const float4*>(&meta.k[i]);
+        x[i] = fmaf(__uint_as_float(i < 32 ? s0[i & 31] : s1[i & 31]), km.x, km.y * qsum);
+        x[i + 1] = fmaf(__uint_as_float(i < 32 ? s0[(i + 1) & 31] : s1[(i + 1) & 31]), km.z, km.w * qsum);
+      }
+      if (masked) {
+        const int hi = meta.ok ? key_hi - key0 : -1, lo = key_lo - key0;
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (i > hi || i < lo) x[i] = -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < 64; ++i) top = fmaxf(top, x[i]);
+      // ---- the reference, and O with it where it moves
+      float f = 1.0f;
+      if (top != -INFINITY) {
+        const float m = top * qc;
+        if (m_ref == -INFINITY) {
+          m_ref = m;  // nothing summed yet
+        } else if (m > m_ref + kLazy) {
+          f = ex2(m_ref - m);
+          m_ref = m;
+          l *= f;
+          z *= f;
+        }
+      }
+      if (grow) f *= pow2(-grow);
+      if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+        if (!mbar_wait(&pv_done[tile], (j - 1) & 1, p.err, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(tmem + lanes + static_cast<uint32_t>(L::o_col(tile) + c), o);
+          tmem_ld_wait();
+          tmem_reg_fence(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+          tmem_st_32x32b_x32(tmem + lanes + static_cast<uint32_t>(L::o_col(tile) + c), o);
+        }
+        tmem_st_wait();
+      }
+      // ---- probabilities, sums, and W over the scores
+      const float ref = m_ref == -INFINITY ? 0.0f : m_ref;
+      uint32_t w0[32], w1[32];
+#pragma unroll
+      for (int i = 0; i < 64; i += 2) {
+        const float4 vm = *reinterpret_cast<const float4*>(&meta.v[i]);
+        float pa = ex2(fmaf(x[i], qc, -ref)), pb = ex2(fmaf(x[i + 1], qc, -ref));
+        float wa = pa * vm.x, wb = pb * vm.z, za = pa * vm.y, zb = pb * vm.w;
+        if (masked) {  // whatever the value row of a masked key holds
+          if (x[i] == -INFINITY) pa = wa = za = 0.0f;
+          if (x[i + 1] == -INFINITY) pb = wb = zb = 0.0f;
+        }
+        l += pa + pb;
+        z += za + zb;
+        w0[i >> 1] = pack_h2(wa, wb);
+        if constexpr (kSplit) {
+          const __half2 h = *reinterpret_cast<const __half2*>(&w0[i >> 1]);
+          w1[i >> 1] = pack_h2(wa - __low2float(h), wb - __high2float(h));
+        }
+      }
+      tmem_st_32x32b_x32(s_addr, w0);
+      if constexpr (kSplit) tmem_st_32x32b_x32(s_addr + 32, w1);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&p_full[tile]);
+        mbar_arrive(&meta_empty[ms]);
+      }
+    }
+    // ---- the row's result
+    if (ok && (pages == 0 || mbar_wait(&pv_done[tile], (pages - 1) & 1, p.err, abort_flag))) {
+      tc_fence_after();
+      const float un_w = pow2(e_run - kWExp);
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // no key seen: zeros; NaN stays
+      const bool any_on = tile_r0 + 32 * (warp & 3) < rows;
+      if (any_on) {
+#pragma unroll 1
+        for (int a = 0; a < D / 32; ++a) {
+          // dimensions 32 a ..: columns d (D / 8) + 4 a .. + 3 hold dimension d of the groups of 8
+          uint32_t o[32];
+          if (pages > 0) {
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+              tmem_ld_32x32b_x4(tmem + lanes + static_cast<uint32_t>(L::o_col(tile) + d * (D / 8) + 4 * a), o + 4 * d);
+            tmem_ld_wait();
+            tmem_reg_fence(o);
+          }
+          if (!row_on) continue;
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int d = 0; d < 8; ++d) v[8 * k + d] = pages > 0 ? fmaf(__uint_as_float(o[4 * d + k]), un_w, z) : 0.0f;
+          if (p.part) {
+            float* dst = p.part + (static_cast<int64_t>(blockIdx.z) * p.T * p.Hq + q_at) * (D + 4) + 32 * a;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<float4*>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else {
+            OT* dst = out + q_at * D + 32 * a;
+            constexpr int kPer = 16 / static_cast<int>(sizeof(OT));
+#pragma unroll
+            for (int i = 0; i < 32 / kPer; ++i) {
+              union { OT v[kPer]; uint4 u; } pk;
+#pragma unroll
+              for (int k = 0; k < kPer; ++k) pk.v[k] = round_out<OT>(v[i * kPer + k] * inv);
+              reinterpret_cast<uint4*>(dst)[i] = pk.u;
+            }
+          }
+        }
+        if (p.part && row_on)
+          *reinterpret_cast<float2*>(p.part + (static_cast<int64_t>(blockIdx.z) * p.T * p.Hq + q_at) * (D + 4) + D) =
+              make_float2(m_ref, l);
+      }
+    }
+  } else if (warp < L::kProducer) {
+    // ------------------------------------------------------------ unpack
+    const int ut = threadIdx.x - 32 * L::kSoftWarps;  // 0 .. 127
+    constexpr int kWords = D / 8;                     // words of a row
+    int e_run = -1000;
+    for (int j = 0; j < pages; ++j) {
+      const int rs = j % L::kRaw, ks = j % L::kK, vs = j % L::kV, ms = j % L::kMeta;
+      if (!mbar_wait(&raw_full[rs], (j / L::kRaw) & 1, p.err, abort_flag)) break;
+      const uint8_t* raw = smem + L::offRaw + rs * B::kBytes;
+      const int page = p.c.page_table[static_cast<int64_t>(b) * p.c.max_pages + page0 + j];
+      const bool ok = page >= 0 && page < p.c.num_pages;
+      // ---- keys: a word (8 dimensions) to a 16-byte chunk of the key's operand row
+      if (!mbar_wait(&k_empty[ks], ((j / L::kK) & 1) ^ 1, p.err, abort_flag)) break;
+      uint8_t* kop = smem + L::offK + ks * L::kOp;
+#pragma unroll 4
+      for (int i = 0; i < kKvPage * kWords / 128; ++i) {
+        const int id = i * 128 + ut, w = id % kWords, key = id / kWords;
+        const uint32_t a = ok ? *reinterpret_cast<const uint32_t*>(raw + B::offK + key * B::kRow + 4 * w) : 0x88888888u;
+        const uint32_t a8 = a >> 8;
+        *reinterpret_cast<uint4*>(kop + (w >> 3) * (kKvPage * 128) + (key >> 3) * 1024 + (key & 7) * 128 +
+                                  (((w & 7) ^ (key & 7)) << 4)) =
+            make_uint4(codes_lo(a), codes_hi(a), codes_lo(a8), codes_hi(a8));
+      }
+      // ---- factors
+      if (!mbar_wait(&meta_empty[ms], ((j / L::kMeta) & 1) ^ 1, p.err, abort_flag)) break;
+      {
+        // every warp needs the page's largest value scale (of tokens that exist)
+        const float2* vmeta = reinterpret_cast<const float2*>(raw + B::offVMeta);
+        const int key0 = (page0 + j) * kKvPage;
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (ok && key0 + lane + 32 * i < len) top = fmaxf(top, vmeta[lane + 32 * i].x);
+        top = warp_max(top);
+        const int e_pg = pow2_exp(top);
+        int grow = 0;
+        if (e_run == -1000) {
+          e_run = e_pg + 1;  // some room, so that it seldom moves
+        } else if (e_pg > e_run) {
+          grow = e_pg + 1 - e_run;
+          e_run = e_pg + 1;
+        }
+        PageMeta& meta = metas[ms];
+        const float f = pow2(kWExp - e_run);
+        const bool is_v = ut >= kKvPage;
+        const int key = ut & (kKvPage - 1);
+        const float2 sm = reinterpret_cast<const float2*>(raw + (is_v ? B::offVMeta : B::offKMeta))[key];
+        const float mid = fmaf(8.0f, sm.x, sm.y);
+        if (is_v) meta.v[key] = make_float2(sm.x * f, mid);
+        else meta.k[key] = make_float2(sm.x, mid);
+        if (ut == 0) {
+          meta.key0 = key0;
+          meta.ok = ok ? 1 : 0;
+          meta.grow = grow;
+          meta.e = e_run;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&k_full[ks]);
+        mbar_arrive(&meta_full[ms]);
+      }
+      // ---- values, transposed: a word of 8 consecutive keys to 8 chunks, one per dimension; dimension 8 w + d is
+      // operand row d (D / 8) + w, so that a warp's chunks of one d lie in consecutive rows (different banks)
+      if (!mbar_wait(&v_empty[vs], ((j / L::kV) & 1) ^ 1, p.err, abort_flag)) break;
+      uint8_t* vop = smem + L::offV + vs * L::kOp;
+#pragma unroll 1
+      for (int i = 0; i < 8 * kWords / 128; ++i) {
+        const int id = i * 128 + ut, w = id % kWords, kg = id / kWords;
+        uint32_t a[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          a[k] = ok ? *reinterpret_cast<const uint32_t*>(raw + B::offV + (8 * kg + k) * B::kRow + 4 * w) : 0x88888888u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t sel = c | ((4 + c) << 8);
+          uint32_t pr[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) pr[k] = prmt_b32(a[2 * k], a[2 * k + 1], sel);
+          const int n0 = 2 * c * kWords + w, n1 = n0 + kWords;
+          *reinterpret_cast<uint4*>(vop + (n0 >> 3) * 1024 + (n0 & 7) * 128 + ((kg ^ (n0 & 7)) << 4)) =
+              make_uint4(codes_lo(pr[0]), codes_lo(pr[1]), codes_lo(pr[2]), codes_lo(pr[3]));
+          *reinterpret_cast<uint4*>(vop + (n1 >> 3) * 1024 + (n1 & 7) * 128 + ((kg ^ (n1 & 7)) << 4)) =
+              make_uint4(codes_hi(pr[0]), codes_hi(pr[1]), codes_hi(pr[2]), codes_hi(pr[3]));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&v_full[vs]);
+        mbar_arrive(&raw_empty[rs]);
+      }
+    }
+  } else if (warp == L::kProducer) {
+    // ------------------------------------------------------------ raw pages
+    if (lane == 0) {
+      int j = 0;
+      for (; j < pages; ++j) {
+        const int rs = j % L::kRaw;
+        const int page = p.c.page_table[static_cast<int64_t>(b) * p.c.max_pages + page0 + j];
+        if (!mbar_wait(&raw_empty[rs], ((j / L::kRaw) & 1) ^ 1, p.err, abort_flag)) break;
+        if (page < 0 || page >= p.c.num_pages) {
+          atomicOr(p.err, kErrBadIndex);
+          mbar_arrive(&raw_full[rs]);
+        } else {
+          mbar_arrive_expect_tx(&raw_full[rs], B::kBytes);
+          bulk_load(smem + L::offRaw + rs * B::kBytes,
+                    p.c.cache + (static_cast<int64_t>(page) * p.c.heads + head) * B::kBytes, B::kBytes, &raw_full[rs]);
+        }
+      }
+      if (*abort_flag)  // given up: copies still in flight must land before the CTA's shared memory goes
+        for (int i = max(0, j - L::kRaw); i < j; ++i) mbar_wait(&raw_full[i % L::kRaw], (i / L::kRaw) & 1, p.err);
+    }
+  } else {
+    // ------------------------------------------------------------ MMA issue, a warp per tile
+    if (lane == 0) {
+      const int t = warp - L::kMma0;
+      constexpr uint32_t id_s = idesc_f16_f32(kRows, kKvPage), id_o = idesc_f16_f32(kRows, D);
+      const uint32_t q_addr = smem_u32(smem + L::offQ + t * L::kParts * L::kQPart);
+      auto scores = [&](int j) {
+        const int ks = j % L::kK;
+        if (!mbar_wait(&k_full[ks], (j / L::kK) & 1, p.err, abort_flag)) return false;
+        tc_fence_after();
+        const uint32_t k_addr = smem_u32(smem + L::offK + ks * L::kOp);
+        const uint32_t d = tmem + static_cast<uint32_t>(L::s_col(t, j & 1));
+#pragma unroll
+        for (int part = 0; part < L::kParts; ++part)
+#pragma unroll
+          for (int s = 0; s < D / 64; ++s)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma_f16(d, sw128_kmajor_desc(q_addr + part * L::kQPart + s * (kRows * 128)) + 2 * k,
+                         sw128_kmajor_desc(k_addr + s * (kKvPage * 128)) + 2 * k, id_s, (part | s | k) != 0 ? 1u : 0u);
+        tc_commit(&s_full[2 * t + (j & 1)]);
+        tc_commit(&k_empty[ks]);
+        return true;
+      };
+      bool ok = pages == 0 || scores(0);
+      for (int j = 0; ok && j < pages; ++j) {
+        if (j + 1 < pages) {
+          // the other score buffer holds W of the page before: its product must be done with it
+          if (j > 0 && !mbar_wait(&pv_done[t], (j - 1) & 1, p.err, abort_flag)) break;
+          if (!scores(j + 1)) break;
+        }
+        const int vs = j % L::kV;
+        if (!mbar_wait(&v_full[vs], (j / L::kV) & 1, p.err, abort_flag)) break;
+        if (!mbar_wait(&p_full[t], j & 1, p.err, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t v_addr = smem_u32(smem + L::offV + vs * L::kOp);
+#pragma unroll
+        for (int part = 0; part < L::kParts; ++part)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_f16_ta(tmem + static_cast<uint32_t>(L::o_col(t)),
+                          tmem + static_cast<uint32_t>(L::s_col(t, j & 1) + 32 * part + 8 * k),
+                          sw128_kmajor_desc(v_addr) + 2 * k, id_o, (j | part | k) != 0 ? 1u : 0u);
+        tc_commit(&pv_done[t]);
+        tc_commit(&v_empty[vs]);
+      }
+      if (*abort_flag) {  // given up: the products in flight must end before shared and tensor memory go
+        tc_commit(&drained[t]);
+        mbar_wait(&drained[t], 0, p.err);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == L::kMma0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kCols);
+  }
+}
+
+// Joins the page ranges of a row, in order: a warp per (row, query head).
+template <int D, typename OT>
+__global__ void __launch_bounds__(128) k_kv4_join_rows(const Problem p, int splits, OT* __restrict__ out) {
+  constexpr int kPer = D / 32;
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int64_t all = static_cast<int64_t>(p.T) * p.Hq;
+  if (row >= all) return;
+  const int b = kv_seq_of_row(p.c.q_start, p.c.num_seqs, static_cast<int>(row / p.Hq), lane);
+  if (b < 0) return;
+  const int q0 = p.c.q_start[b];
+  const int64_t n = static_cast<int64_t>(p.c.q_start[b + 1]) - q0;
+  if (n < 0 || n > p.max_q || q0 < 0 || q0 + n > p.T) return;  // left out, as its scores were
+  const float* src = p.part + row * (D + 4);
+  const int64_t stride = all * (D + 4);
+  float m = -INFINITY, l = 0.0f, o[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[i] = 0.0f;
+  for (int s = 0; s < splits; ++s) m = fmaxf(m, src[s * stride + D]);
+  if (m == -INFINITY) m = 0.0f;
+  for (int s = 0; s < splits; ++s) {
+    const float2 ml = *reinterpret_cast<const float2*>(src + s * stride + D);
+    const float f = ex2(ml.x - m);
+    l = fmaf(f, ml.y, l);
+#pragma unroll
+    for (int i = 0; i < kPer / 4; ++i) {
+      const float4 v = reinterpret_cast<const float4*>(src + s * stride)[32 * i + lane];
+      o[4 * i] = fmaf(f, v.x, o[4 * i]);
+      o[4 * i + 1] = fmaf(f, v.y, o[4 * i + 1]);
+      o[4 * i + 2] = fmaf(f, v.z, o[4 * i + 2]);
+      o[4 * i + 3] = fmaf(f, v.w, o[4 * i + 3]);
+    }
+  }
+  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+#pragma unroll
+  for (int i = 0; i < kPer / 4; ++i) {
+    union { OT v[4]; uint2 u2; uint4 u4; } pk;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) pk.v[c] = round_out<OT>(o[4 * i + c] * inv);
+    OT* dst = out + row * D + 128 * i + 4 * lane;
+    if constexpr (sizeof(OT) == 4) *reinterpret_cast<uint4*>(dst) = pk.u4;
+    else *reinterpret_cast<uint2*>(dst) = pk.u2;
+  }
+}
+
+template <int D, typename QT, typename OT>
+cudaError_t launch_t(DeviceContext* ctx, Problem p, const void* q, void* out, cudaStream_t s, int* status) {
+  constexpr bool kSplit = std::is_same<QT, float>::value;
+  using L = Layout<D, kSplit>;
+  // units of kT * 128 rows: any division of T rows into sequences of at most max_q has at most this many
+  const int64_t per = L::kT * kRows;
+  const int64_t units = static_cast<int64_t>(p.T) * p.G / per + (p.c.num_seqs < p.T ? p.c.num_seqs : p.T);
+  if (units * p.c.heads > 0x7fffffff) {
+    *status = BITNET_ERR_UNSUPPORTED_SHAPE;
+    return cudaSuccess;
+  }
+  // Too few units for the SMs: split the pages, at least 8 to a part.
+  int64_t splits = 1;
+  if (units * p.c.heads < ctx->num_sms) splits = ctx->num_sms / (units * p.c.heads);
+  const int64_t most = (p.c.max_pages + 7) / 8;
+  if (splits > most) splits = most;
+  if (splits > 64) splits = 64;
+  uint8_t* ws = nullptr;
+  if (splits > 1) {
+    const size_t bytes = static_cast<size_t>(splits) * p.T * p.Hq * (D + 4) * 4;
+    if ((*status = pool_alloc(ctx, reinterpret_cast<void**>(&ws), bytes, s))) return cudaSuccess;
+    p.part = reinterpret_cast<float*>(ws);
+  }
+  auto kern = k_kv4_prefill<D, kSplit, QT, OT>;
+  cudaError_t e = allow_smem(ctx, reinterpret_cast<const void*>(kern), L::kAlloc);
+  if (e == cudaSuccess) {
+    kern<<<dim3(static_cast<unsigned>(units * p.c.heads), 1, static_cast<unsigned>(splits)), L::kThreads, L::kAlloc, s>>>(
+        p, static_cast<const QT*>(q), static_cast<OT*>(out));
+    e = cudaGetLastError();
+  }
+  if (splits > 1) {
+    if (e == cudaSuccess) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(p.T) * p.Hq + 3) / 4));
+      cfg.blockDim = dim3(128);
+      cfg.stream = s;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaLaunchKernelEx(&cfg, k_kv4_join_rows<D, OT>, static_cast<const Problem>(p), static_cast<int>(splits),
+                             static_cast<OT*>(out));
+    }
+    pool_free(ws, s);
+  }
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_prefill(DeviceContext* ctx, const KvView& c, int head_dim, const void* q, int q_dtype, int64_t T,
+                               int Hq, int max_q_len, float scale, int causal, int window, void* out, int out_dtype,
+                               cudaStream_t s, int* status) {
+  Problem p = {};
+  p.c = c;
+  p.Hq = Hq;
+  p.G = Hq / c.heads;
+  p.T = static_cast<int>(T);
+  p.max_q = max_q_len;
+  p.scale = fabsf(scale) * 1.4426950408889634f;
+  p.sign = scale < 0.0f ? -1.0f : 1.0f;
+  p.causal = causal;
+  p.window = window < (1 << 30) ? window : 1 << 30;  // keeps position - window within 32 bits
+  p.err = ctx->err_word;
+  if (T * p.G > 0x3fffffff) {  // rows of an item are counted in 32 bits
+    *status = BITNET_ERR_UNSUPPORTED_SHAPE;
+    return cudaSuccess;
+  }
+  auto go = [&](auto* qt, auto* ot) {
+    using QT = std::remove_pointer_t<decltype(qt)>;
+    using OT = std::remove_pointer_t<decltype(ot)>;
+    return head_dim == 128 ? launch_t<128, QT, OT>(ctx, p, q, out, s, status)
+                           : launch_t<256, QT, OT>(ctx, p, q, out, s, status);
+  };
+  float* f = nullptr;
+  __half* h = nullptr;
+  __nv_bfloat16* bf = nullptr;
+  const bool f32_out = out_dtype == BITNET_DTYPE_F32;
+  switch (q_dtype) {
+    case BITNET_DTYPE_F32: return go(f, f);
+    case BITNET_DTYPE_F16: return f32_out ? go(h, f) : go(h, h);
+    case BITNET_DTYPE_BF16: return f32_out ? go(bf, f) : go(bf, bf);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace bitnet
