@@ -67,8 +67,17 @@ int bitnet_w8a8_gemm(const int8_t* a_codes, const float* a_scale, const int8_t* 
     return BITNET_ERR_MISALIGNED;
   DeviceContext* ctx;
   if ((rc = device_context(&ctx))) return rc;
-  return cuda_status(launch_w8a8(ctx, a_codes, a_scale, w_codes, w_scale, M, K, N, y, y_dtype, acc_out,
-                                 reinterpret_cast<cudaStream_t>(stream)));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (w8a8_few_supported(M))
+    return cuda_status(launch_w8a8_few(ctx, a_codes, a_scale, w_codes, w_scale, M, K, N, y, y_dtype, acc_out, false, s));
+  __half* f16 = nullptr;
+  if ((rc = pool_alloc(ctx, reinterpret_cast<void**>(&f16), static_cast<size_t>(M * K) * 2, s))) return rc;
+  int st = BITNET_OK;
+  cudaError_t e = launch_w8a8_codes(a_codes, f16, M * K, s);
+  if (e == cudaSuccess)
+    e = launch_w8a8_tc(ctx, f16, a_scale, w_codes, w_scale, M, K, N, y, y_dtype, acc_out, true, s, &st);
+  pool_free(f16, s);
+  return st != BITNET_OK ? st : cuda_status(e);
 }
 
 int bitnet_w8a8_forward(const void* x, int x_dtype, const float* norm_w, const int8_t* w_codes, const float* w_scale,
@@ -83,15 +92,28 @@ int bitnet_w8a8_forward(const void* x, int x_dtype, const float* norm_w, const i
   DeviceContext* ctx;
   if ((rc = device_context(&ctx))) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const size_t code_bytes = (static_cast<size_t>(M * K) + 255) & ~size_t(255);
+  const bool few = w8a8_few_supported(M);
+  const size_t code_bytes = (static_cast<size_t>(M * K) * (few ? 1 : 2) + 255) & ~size_t(255);
   uint8_t* ws = nullptr;
   if ((rc = pool_alloc(ctx, reinterpret_cast<void**>(&ws), code_bytes + static_cast<size_t>(M) * 4, s))) return rc;
-  int8_t* codes = reinterpret_cast<int8_t*>(ws);
   float* as = reinterpret_cast<float*>(ws + code_bytes);
-  cudaError_t e = launch_rmsnorm_quant_i8_in(x, x_dtype, norm_w, M, static_cast<int>(K), eps, codes, as, false, s);
-  if (e == cudaSuccess) e = launch_w8a8(ctx, codes, as, w_codes, w_scale, M, K, N, y, y_dtype, nullptr, s);
+  // the norm launch waits for what is before it, so the contraction, which may start during it, may read weights
+  const int k = static_cast<int>(K);
+  int st = BITNET_OK;
+  cudaError_t e;
+  if (few) {
+    int8_t* codes = reinterpret_cast<int8_t*>(ws);
+    e = launch_rmsnorm_quant_i8_in(x, x_dtype, norm_w, M, k, eps, codes, as, false, s);
+    if (e == cudaSuccess)
+      e = launch_w8a8_few(ctx, codes, as, w_codes, w_scale, M, K, N, y, y_dtype, nullptr, true, s);
+  } else {
+    __half* codes = reinterpret_cast<__half*>(ws);
+    e = launch_rmsnorm_quant_f16_in(x, x_dtype, norm_w, M, k, eps, codes, as, false, s);
+    if (e == cudaSuccess)
+      e = launch_w8a8_tc(ctx, codes, as, w_codes, w_scale, M, K, N, y, y_dtype, nullptr, true, s, &st);
+  }
   pool_free(ws, s);
-  return cuda_status(e);
+  return st != BITNET_OK ? st : cuda_status(e);
 }
 
 size_t bitnet_kv4_cache_bytes(int64_t num_pages, int32_t num_kv_heads, int32_t head_dim) {

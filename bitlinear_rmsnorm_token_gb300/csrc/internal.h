@@ -170,9 +170,17 @@ cudaError_t launch_rmsnorm_quant_i8_in(const void* x, int x_dtype, const float* 
 // 8-bit weights: per-channel quantisation, and the int8 x int8 contraction on
 // int8 activation codes.
 cudaError_t launch_quant_w8(const float* w, int64_t N, int64_t K, int8_t* codes, float* scale, cudaStream_t s);
-cudaError_t launch_w8a8(DeviceContext* ctx, const int8_t* a, const float* a_scale, const int8_t* w,
-                        const float* w_scale, int64_t M, int64_t K, int64_t N, void* y, int y_dtype, int32_t* acc_out,
-                        cudaStream_t s);
+// Few tokens on int8 codes, more on fp16 codes (launch_w8a8_codes turns one into
+// the other).  pdl: launched to overlap the launch before it, which writes the
+// codes and scales but no weights.
+bool w8a8_few_supported(int64_t M);
+cudaError_t launch_w8a8_few(const DeviceContext* ctx, const int8_t* a, const float* a_scale, const int8_t* w,
+                            const float* w_scale, int64_t M, int64_t K, int64_t N, void* y, int y_dtype,
+                            int32_t* acc_out, bool pdl, cudaStream_t s);
+cudaError_t launch_w8a8_codes(const int8_t* codes, __half* out, int64_t count, cudaStream_t s);
+cudaError_t launch_w8a8_tc(const DeviceContext* ctx, const __half* codes, const float* a_scale, const int8_t* w,
+                           const float* w_scale, int64_t M, int64_t K, int64_t N, void* y, int y_dtype,
+                           int32_t* acc_out, bool pdl, cudaStream_t s, int* status);
 
 // The paged 4-bit key/value cache (kv4.cuh): head_dim 128 or 256.
 struct KvView;

@@ -47,6 +47,17 @@ __device__ __forceinline__ uint32_t prmt_b32(uint32_t a, uint32_t b, uint32_t se
   return d;
 }
 
+// Four int8 codes -> two half2 words holding their values: 0x6400 | u is 1024 +
+// u, with u = code + 128, minus 1152.
+__device__ __forceinline__ void int8_to_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u, kMagic = 0x64646464u, kBias = 0x64806480u;  // half2(1152, 1152)
+  const uint32_t a = prmt_b32(u, kMagic, 0x4140u), b = prmt_b32(u, kMagic, 0x4342u);
+  const __half2 ha = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&kBias));
+  const __half2 hb = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&kBias));
+  lo = *reinterpret_cast<const uint32_t*>(&ha);
+  hi = *reinterpret_cast<const uint32_t*>(&hb);
+}
+
 // 1.5 * 2^23: adding it to a float of magnitude below 2^22 rounds that float to
 // an integer (ties to even, like rintf) held in the low mantissa bits.
 constexpr float kRoundMagic = 12582912.0f;

@@ -1,5 +1,14 @@
-// w8a8.cu -- projections with 8-bit weights: per-channel weight quantisation
-// and the int8 x int8 contraction.
+// w8a8.cu -- projections with 8-bit weights: per-channel weight quantisation,
+// the few-token contraction, and which contraction a token count takes.
+//
+// acc[m, n] = sum_k a[m, k] w[n, k] in int32, y = ((float)acc * (1 / a_scale[m]))
+// * (1 / w_scale[n]) with every operation rounded on its own.
+//
+// Up to 8 tokens the weights' N K bytes are all that counts: a warp streams kR
+// rows of them with 16-byte loads, many in flight, and multiplies with dp4a (4
+// products an instruction and token) against the codes, which stay in L1.  The
+// first loads of a warp are issued before the wait for the launch that writes
+// the codes.  From 9 tokens on the tensor cores (w8a8_tc.cu) take over.
 #include "common.cuh"
 #include "internal.h"
 #include "rowquant.cuh"
@@ -38,35 +47,121 @@ __global__ void __launch_bounds__(kWarps * 32) k_quant_w8(const float* __restric
   if (lane == 0) scale[n] = sc;
 }
 
-// A warp per output: 16-byte chunks of the two rows, dp4a.
-template <typename YT>
-__global__ void __launch_bounds__(kWarps * 32) k_w8a8_dot(const int8_t* __restrict__ a,
+__device__ __forceinline__ void store_y(void* y, int y_dtype, int64_t at, float v) {
+  if (y_dtype == BITNET_DTYPE_F32) static_cast<float*>(y)[at] = v;
+  else if (y_dtype == BITNET_DTYPE_F16) static_cast<__half*>(y)[at] = round_out<__half>(v);
+  else static_cast<__nv_bfloat16*>(y)[at] = round_out<__nv_bfloat16>(v);
+}
+
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {  // read once: not kept in L1
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// A warp takes kR consecutive rows; kM tokens (rows past M repeat the last and
+// are not stored).  Chunk i of a row is its bytes 512 i + 16 lane ...
+template <int kM, int kR>
+__global__ void __launch_bounds__(kWarps * 32) k_w8a8_few(const int8_t* __restrict__ a,
                                                           const float* __restrict__ a_scale,
                                                           const int8_t* __restrict__ w,
                                                           const float* __restrict__ w_scale, int M, int N, int K,
-                                                          YT* __restrict__ y, int32_t* __restrict__ acc_out) {
+                                                          void* __restrict__ y, int y_dtype,
+                                                          int32_t* __restrict__ acc_out) {
+  constexpr int kAhead = kR == 4 ? 4 : 8;  // chunks of every row in flight
   const int lane = threadIdx.x & 31;
-  const int n = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (n >= N) return;
-  const uint4* wr = reinterpret_cast<const uint4*>(w + static_cast<int64_t>(n) * K);
-  const float inv_w = __frcp_rn(w_scale[n]);
-  for (int m = blockIdx.y; m < M; m += gridDim.y) {
-    const uint4* ar = reinterpret_cast<const uint4*>(a + static_cast<int64_t>(m) * K);
-    int acc = 0;
-    for (int i = lane; i < K / 16; i += 32) {
-      const uint4 x = __ldg(wr + i), v = __ldg(ar + i);
-      acc = __dp4a(static_cast<int>(x.x), static_cast<int>(v.x), acc);
-      acc = __dp4a(static_cast<int>(x.y), static_cast<int>(v.y), acc);
-      acc = __dp4a(static_cast<int>(x.z), static_cast<int>(v.z), acc);
-      acc = __dp4a(static_cast<int>(x.w), static_cast<int>(v.w), acc);
+  const int n0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kR;
+  const int chunks = (K + 511) / 512;
+  const uint4* wr[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r)
+    wr[r] = reinterpret_cast<const uint4*>(w + static_cast<int64_t>(min(n0 + r, N - 1)) * K) + lane;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  int acc[kM][kR];
+#pragma unroll
+  for (int m = 0; m < kM; ++m)
+#pragma unroll
+    for (int r = 0; r < kR; ++r) acc[m][r] = 0;
+  bool waited = false;
+  for (int c0 = 0; c0 < chunks; c0 += kAhead) {
+    uint4 wv[kAhead][kR];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const bool in = (c0 + i) * 512 + lane * 16 < K;
+#pragma unroll
+      for (int r = 0; r < kR; ++r) wv[i][r] = in ? ld_stream(wr[r] + (c0 + i) * 32) : zero;
     }
-    acc = warp_sum_int(acc);
-    if (lane == 0) {
-      const int64_t at = static_cast<int64_t>(m) * N + n;
-      y[at] = round_out<YT>(rescale_elem(static_cast<float>(acc), __frcp_rn(a_scale[m]), inv_w));
-      if (acc_out) acc_out[at] = acc;
+    if (!waited) {
+      pdl_wait();  // the codes come from the launch before this one
+      waited = true;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = (c0 + i) * 512 + lane * 16;
+      if (k >= K) break;
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        const uint4 v = *reinterpret_cast<const uint4*>(a + static_cast<int64_t>(min(m, M - 1)) * K + k);
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+          acc[m][r] = __dp4a(static_cast<int>(wv[i][r].x), static_cast<int>(v.x), acc[m][r]);
+          acc[m][r] = __dp4a(static_cast<int>(wv[i][r].y), static_cast<int>(v.y), acc[m][r]);
+          acc[m][r] = __dp4a(static_cast<int>(wv[i][r].z), static_cast<int>(v.z), acc[m][r]);
+          acc[m][r] = __dp4a(static_cast<int>(wv[i][r].w), static_cast<int>(v.w), acc[m][r]);
+        }
+      }
     }
   }
+#pragma unroll
+  for (int m = 0; m < kM; ++m)
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const int sum = warp_sum_int(acc[m][r]);
+      if (lane == (m * kR + r) % 32 && m < M && n0 + r < N) {
+        const int64_t at = static_cast<int64_t>(m) * N + n0 + r;
+        store_y(y, y_dtype, at,
+                rescale_elem(static_cast<float>(sum), __frcp_rn(a_scale[m]), __frcp_rn(__ldg(w_scale + n0 + r))));
+        if (acc_out) acc_out[at] = sum;
+      }
+    }
+}
+
+// int8 codes as fp16 (exact), 16 a thread.
+__global__ void __launch_bounds__(256) k_w8a8_codes(const int8_t* __restrict__ in, __half* __restrict__ out,
+                                                    int64_t n16) {
+  pdl_launch_dependents();
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (t >= n16) return;
+  const uint4 v = __ldg(reinterpret_cast<const uint4*>(in) + t);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) int8_to_h2(w[i], o[2 * i], o[2 * i + 1]);
+  uint4* dst = reinterpret_cast<uint4*>(out) + 2 * t;
+  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+template <int kM>
+cudaError_t launch_few(const DeviceContext* ctx, const int8_t* a, const float* a_scale, const int8_t* w,
+                       const float* w_scale, int M, int N, int K, void* y, int y_dtype, int32_t* acc_out, bool pdl,
+                       cudaStream_t s) {
+  // rows per warp: as many as leave every SM eight warps
+  const int64_t warps = static_cast<int64_t>(ctx->num_sms) * kWarps;
+  const int kr = N >= 4 * warps && kM > 2 ? 4 : (N >= 2 * warps ? 2 : 1);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(N) + kr * kWarps - 1) / (kr * kWarps)));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto kern = kr == 4 ? k_w8a8_few<kM, 4> : (kr == 2 ? k_w8a8_few<kM, 2> : k_w8a8_few<kM, 1>);
+  return cudaLaunchKernelEx(&cfg, kern, a, a_scale, w, w_scale, M, N, K, y, y_dtype, acc_out);
 }
 
 }  // namespace
@@ -77,25 +172,22 @@ cudaError_t launch_quant_w8(const float* w, int64_t N, int64_t K, int8_t* codes,
   return cudaGetLastError();
 }
 
-cudaError_t launch_w8a8(DeviceContext* ctx, const int8_t* a, const float* a_scale, const int8_t* w,
-                        const float* w_scale, int64_t M, int64_t K, int64_t N, void* y, int y_dtype, int32_t* acc_out,
-                        cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((N + kWarps - 1) / kWarps), static_cast<unsigned>(M < 1024 ? M : 1024));
+bool w8a8_few_supported(int64_t M) { return M <= 8; }
+
+cudaError_t launch_w8a8_few(const DeviceContext* ctx, const int8_t* a, const float* a_scale, const int8_t* w,
+                            const float* w_scale, int64_t M, int64_t K, int64_t N, void* y, int y_dtype,
+                            int32_t* acc_out, bool pdl, cudaStream_t s) {
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
-  switch (y_dtype) {
-    case BITNET_DTYPE_F32:
-      k_w8a8_dot<<<grid, kWarps * 32, 0, s>>>(a, a_scale, w, w_scale, m, n, k, static_cast<float*>(y), acc_out);
-      break;
-    case BITNET_DTYPE_F16:
-      k_w8a8_dot<<<grid, kWarps * 32, 0, s>>>(a, a_scale, w, w_scale, m, n, k, static_cast<__half*>(y), acc_out);
-      break;
-    case BITNET_DTYPE_BF16:
-      k_w8a8_dot<<<grid, kWarps * 32, 0, s>>>(a, a_scale, w, w_scale, m, n, k, static_cast<__nv_bfloat16*>(y),
-                                              acc_out);
-      break;
-    default:
-      return cudaErrorInvalidValue;
-  }
+  auto go = [&](auto f) { return f(ctx, a, a_scale, w, w_scale, m, n, k, y, y_dtype, acc_out, pdl, s); };
+  if (M == 1) return go(launch_few<1>);
+  if (M == 2) return go(launch_few<2>);
+  if (M <= 4) return go(launch_few<4>);
+  return go(launch_few<8>);
+}
+
+cudaError_t launch_w8a8_codes(const int8_t* codes, __half* out, int64_t count, cudaStream_t s) {
+  const int64_t n16 = count / 16;  // K is a multiple of 128
+  k_w8a8_codes<<<static_cast<unsigned>((n16 + 255) / 256), 256, 0, s>>>(codes, out, n16);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,483 @@
+// w8a8_tc.cu -- int8 x int8 contraction for 9 tokens and more on the
+// 5th-generation tensor cores.
+//
+// acc[m, n] = sum_k a[m, k] w[n, k].  sm_103a has no integer tcgen05 MMA; int8
+// values are exact in fp16, their products in fp32, and a sum of 1024 of them is
+// below 2^14 x 2^10 = 2^24, so the fp32 accumulator holds 1024 of K exactly.
+// K goes in chunks of 1024: two accumulators in turn, the finished one read out
+// and added up as int32 while the other is filled.
+//
+// The weights are the MMA's M side (128 output channels per tile) and come from
+// tensor memory: 4 warps turn a tile's int8 rows into fp16 straight into TMEM
+// columns (a lane is a channel), so the operand costs shared memory only its
+// int8 bytes, once in and once out.  The tokens' fp16 codes are the N side, BN
+// of them per tile, in shared memory by TMA.  Per 64 of K a tile moves 256 BN +
+// 16384 bytes of shared memory against 2 BN cycles of MMA: shared memory (128
+// bytes a cycle) is the bound from BN = 64 on, at 3/4 of the MMA rate for BN =
+// 192, and the weight stream for few tokens.
+//
+//   warps 0-3   unpack: lane quadrant q, one weight row a thread
+//   warps 4-11  epilogue: quadrant warp & 3, half of the tile's tokens each
+//   warp 12     TMA of raw weights (128 rows x 128 bytes, 128B swizzle)
+//   warp 13     TMA of token codes (64 of K per stage)
+//   warp 14     TMEM, MMA issue
+// Few tiles (short or narrow problems): a cluster of S CTAs takes a tile, each a
+// range of K, and adds the parts up through distributed shared memory (int32:
+// the order does not matter).
+// Every wait is bounded; an expired wait sets the device error word and the CTA
+// unwinds without trapping.
+#include <cooperative_groups.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+#include "rowquant.cuh"
+
+namespace bitnet {
+namespace {
+
+constexpr int kBM = 128;            // channels per tile
+constexpr int kRawBytes = kBM * 128;  // a raw slot: 128 rows x 128 of K
+constexpr int kAStageCols = 32;     // TMEM columns of 64 fp16 of K
+constexpr int kChunk = 8;           // K blocks of 128 per exact accumulation
+constexpr int kUnpackWarps = 4, kEpiWarps = 8;
+constexpr int kRawWarp = kUnpackWarps + kEpiWarps, kTokWarp = kRawWarp + 1, kMmaWarp = kRawWarp + 2;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kTmemCols = 512;
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, fp16 operands: A's column c holds K elements 2c, 2c + 1.
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <int BN>
+struct Layout {
+  static constexpr int kTokStage = BN * 128;           // 64 of K
+  static constexpr int kTok = BN == 192 ? 6 : 8;
+  static constexpr int kRaw = BN <= 64 ? 9 : (BN == 128 ? 5 : 4);
+  static constexpr int kAStages = BN == 192 ? 4 : 8;   // TMEM: 2 BN accumulator columns, then these
+  static constexpr int kACol0 = 2 * BN;
+  static constexpr int kEpiCols = BN >= 32 ? BN / 2 : 16;  // token columns per epilogue warp
+  static constexpr int kEpiOn = 4 * (BN / kEpiCols);       // epilogue warps with columns
+  static constexpr int offTok = 0;
+  static constexpr int offRaw = offTok + kTok * kTokStage;
+  static constexpr int kNumBars = 2 * kTok + 2 * kRaw + 2 * kAStages + 4;
+  static constexpr int offBar = offRaw + kRaw * kRawBytes;
+  static constexpr int offMisc = offBar + kNumBars * 8;
+  static constexpr int kBytes = offMisc + 32;
+  static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 232448, "over the 227 KB of shared memory a CTA may use");
+  static_assert(kACol0 + kAStages * kAStageCols <= kTmemCols, "TMEM columns");
+  static_assert(kTok * kTokStage + kRaw * kRawBytes >= BN * kBM * 4, "the split's exchange reuses the rings");
+};
+
+// Tiles in bands of kBand channel tiles, token tiles inside: the CTAs of a wave
+// work on a block of the output, so that both operands are read from L2.
+constexpr int kBand = 12;
+__device__ __forceinline__ void tile_at(int t, int n_wt, int n_mt, int* wt, int* mt) {
+  const int band = t / (kBand * n_mt);
+  const int width = min(kBand, n_wt - band * kBand);
+  const int in = t - band * kBand * n_mt;
+  *mt = in / width;
+  *wt = band * kBand + in - *mt * width;
+}
+
+template <int BN, typename YT>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_w8a8_tc(const __grid_constant__ CUtensorMap tm_tok, const __grid_constant__ CUtensorMap tm_w,
+              const float* __restrict__ a_scale, const float* __restrict__ w_scale, int M, int N, int K, int S,
+              YT* __restrict__ y, int32_t* __restrict__ acc_out, unsigned* err) {
+  using L = Layout<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+  uint64_t* tok_full = reinterpret_cast<uint64_t*>(smem + L::offBar);
+  uint64_t* tok_empty = tok_full + L::kTok;
+  uint64_t* raw_full = tok_empty + L::kTok;
+  uint64_t* raw_empty = raw_full + L::kRaw;
+  uint64_t* a_full = raw_empty + L::kRaw;
+  uint64_t* a_empty = a_full + L::kAStages;
+  uint64_t* acc_full = a_empty + L::kAStages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;          // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::offMisc + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_wt = (N + kBM - 1) / kBM, n_mt = (M + BN - 1) / BN;
+  const int tiles = n_wt * n_mt;
+  const int nkb = K >> 7;
+  const int rank = blockIdx.x % S, first = blockIdx.x / S, step = gridDim.x / S;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / S);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / S);
+  const int blocks = kb1 - kb0;  // K blocks of this CTA, the same for all its tiles (at least one)
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kTok; ++i) {
+      mbar_init(&tok_full[i], 1);
+      mbar_init(&tok_empty[i], 1);
+    }
+    for (int i = 0; i < L::kRaw; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], kUnpackWarps);
+    }
+    for (int i = 0; i < L::kAStages; ++i) {
+      mbar_init(&a_full[i], kUnpackWarps);
+      mbar_init(&a_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], L::kEpiOn);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  int32_t acc[L::kEpiCols];  // epilogue: this thread's channel, its warp's tokens
+
+  if (warp == kRawWarp) {
+    // ------------------------------------------------------------ raw weights
+    // (not written by the launch before this one: no wait for it)
+    if (lane == 0) {
+      int i = 0;
+      for (int t = first; t < tiles; t += step) {
+        int wt, mt;
+        tile_at(t, n_wt, n_mt, &wt, &mt);
+        for (int kb = kb0; kb < kb1; ++kb, ++i) {
+          const int s = i % L::kRaw;
+          if (!mbar_wait(&raw_empty[s], ((i / L::kRaw) & 1) ^ 1, err, abort_flag)) goto raw_done;
+          mbar_arrive_expect_tx(&raw_full[s], kRawBytes);
+          tma_load_2d(smem + L::offRaw + s * kRawBytes, &tm_w, kb * 128, wt * kBM, &raw_full[s]);
+        }
+      }
+    raw_done:
+      if (*abort_flag)  // given up: copies in flight must land before the CTA's shared memory goes
+        for (int k = max(0, i - L::kRaw); k < i; ++k) mbar_wait(&raw_full[k % L::kRaw], (k / L::kRaw) & 1, err);
+    }
+  } else if (warp == kTokWarp) {
+    // ------------------------------------------------------------ token codes
+    if (lane == 0) {
+      pdl_wait();
+      int i = 0;
+      for (int t = first; t < tiles; t += step) {
+        int wt, mt;
+        tile_at(t, n_wt, n_mt, &wt, &mt);
+        for (int h = 0; h < 2 * blocks; ++h, ++i) {
+          const int s = i % L::kTok;
+          if (!mbar_wait(&tok_empty[s], ((i / L::kTok) & 1) ^ 1, err, abort_flag)) goto tok_done;
+          mbar_arrive_expect_tx(&tok_full[s], L::kTokStage);
+          tma_load_2d(smem + L::offTok + s * L::kTokStage, &tm_tok, kb0 * 128 + h * 64, mt * BN, &tok_full[s]);
+        }
+      }
+    tok_done:
+      if (*abort_flag)
+        for (int k = max(0, i - L::kTok); k < i; ++k) mbar_wait(&tok_full[k % L::kTok], (k / L::kTok) & 1, err);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16_f32(kBM, BN);
+      int i = 0, c = 0;  // running stages and chunks
+      for (int t = first; t < tiles; t += step) {
+        for (int h0 = 0; h0 < 2 * blocks; h0 += 2 * kChunk, ++c) {
+          if (!mbar_wait(&acc_empty[c & 1], ((c >> 1) & 1) ^ 1, err, abort_flag)) goto mma_done;
+          tc_fence_after();
+          const uint32_t d = tmem + static_cast<uint32_t>((c & 1) * BN);
+          const int h1 = min(h0 + 2 * kChunk, 2 * blocks);
+          for (int h = h0; h < h1; ++h, ++i) {
+            const int s = i % L::kTok, as = i % L::kAStages;
+            if (!mbar_wait(&tok_full[s], (i / L::kTok) & 1, err, abort_flag)) goto mma_done;
+            if (!mbar_wait(&a_full[as], (i / L::kAStages) & 1, err, abort_flag)) goto mma_done;
+            tc_fence_after();
+            const uint64_t bd = sw128_kmajor_desc(smem_u32(smem + L::offTok + s * L::kTokStage));
+            const uint32_t at = tmem + static_cast<uint32_t>(L::kACol0 + as * kAStageCols);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma_f16_ta(d, at + 8 * k, bd + 2 * k, idesc, (h > h0 || k) ? 1u : 0u);
+            tc_commit(&tok_empty[s]);
+            tc_commit(&a_empty[as]);
+          }
+          tc_commit(&acc_full[c & 1]);
+        }
+      }
+    mma_done:
+      if (*abort_flag) {  // the products in flight must end before shared and tensor memory go
+        // a barrier of its own use: the chunk barriers' phases are unknown here
+        uint64_t* drained = reinterpret_cast<uint64_t*>(smem + L::offMisc + 16);
+        mbar_init(drained, 1);
+        fence_barrier_init();
+        tc_commit(drained);
+        mbar_wait(drained, 0, err);
+      }
+    }
+  } else if (warp < kUnpackWarps) {
+    // ------------------------------------------------------------ unpack
+    const int row = 32 * warp + lane;
+    const uint32_t tq = tmem + (static_cast<uint32_t>(32 * warp) << 16) + static_cast<uint32_t>(L::kACol0);
+    int i = 0, r = 0;  // running stages and raw slots
+    bool pending = false;  // a stage's stores are under way and not yet announced
+    for (int t = first; t < tiles; t += step) {
+      for (int kb = 0; kb < blocks; ++kb, ++r) {
+        const int rs = r % L::kRaw;
+        if (!mbar_wait(&raw_full[rs], (r / L::kRaw) & 1, err, abort_flag)) goto unpack_done;
+        const uint8_t* src = smem + L::offRaw + rs * kRawBytes + row * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h, ++i) {
+          uint32_t cols[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + (((4 * h + c) ^ (row & 7)) << 4));
+            int8_to_h2(v.x, cols[8 * c], cols[8 * c + 1]);
+            int8_to_h2(v.y, cols[8 * c + 2], cols[8 * c + 3]);
+            int8_to_h2(v.z, cols[8 * c + 4], cols[8 * c + 5]);
+            int8_to_h2(v.w, cols[8 * c + 6], cols[8 * c + 7]);
+          }
+          if (h == 1) {  // the slot's bytes are in registers
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_empty[rs]);
+          }
+          // announce the stage before, whose stores ran during this decode
+          if (pending) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&a_full[(i - 1) % L::kAStages]);
+          }
+          const int as = i % L::kAStages;
+          if (!mbar_wait(&a_empty[as], ((i / L::kAStages) & 1) ^ 1, err, abort_flag)) goto unpack_done;
+          tc_fence_after();
+          __syncwarp();
+          tmem_st_32x32b_x32(tq + static_cast<uint32_t>(as * kAStageCols), cols);
+          pending = true;
+        }
+      }
+    }
+    if (pending) {
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&a_full[(i - 1) % L::kAStages]);
+    }
+  unpack_done:;
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int e = warp - kUnpackWarps, q = warp & 3, half = e >> 2;
+    if (e < L::kEpiOn) {
+      pdl_wait();  // the tokens' scales
+      const uint32_t tq = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(half * L::kEpiCols);
+      int c = 0;
+      for (int t = first; t < tiles; t += step) {
+        int wt, mt;
+        tile_at(t, n_wt, n_mt, &wt, &mt);
+        bool ok = true;
+        for (int h0 = 0; h0 < blocks; h0 += kChunk, ++c) {
+          if (!mbar_wait_idle(&acc_full[c & 1], (c >> 1) & 1, err, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < L::kEpiCols; j += 16) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(tq + static_cast<uint32_t>((c & 1) * BN + j), v);
+            tmem_ld_wait();
+            tmem_reg_fence16(v);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int d = __float2int_rn(__uint_as_float(v[k]));
+              acc[j + k] = h0 == 0 ? d : acc[j + k] + d;
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[c & 1]);
+        }
+        if (!ok) break;
+        if (S > 1) break;  // one tile; the parts meet below
+        const int n = wt * kBM + 32 * q + lane, m0 = mt * BN + half * L::kEpiCols;
+        const float inv_w = n < N ? __frcp_rn(__ldg(w_scale + n)) : 0.0f;
+        // the warp's reciprocals, a lane a token
+        float inv[(L::kEpiCols + 31) / 32];
+#pragma unroll
+        for (int j = 0; j < (L::kEpiCols + 31) / 32; ++j) {
+          const int m = m0 + 32 * j + lane;
+          inv[j] = m < M ? __frcp_rn(a_scale[m]) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < L::kEpiCols; ++j) {
+          const float inv_a = __shfl_sync(0xffffffffu, inv[j >> 5], j & 31);
+          if (m0 + j < M && n < N) {
+            const int64_t at = static_cast<int64_t>(m0 + j) * N + n;
+            y[at] = round_out<YT>(rescale_elem(static_cast<float>(acc[j]), inv_a, inv_w));
+            if (acc_out) acc_out[at] = acc[j];
+          }
+        }
+      }
+    }
+  }
+
+  if (S > 1) {
+    // ---- a cluster's parts of one tile: [token][channel] int32 in the rings, which nothing uses any more
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    int32_t* part = reinterpret_cast<int32_t*>(smem);
+    const int e = warp - kUnpackWarps, q = warp & 3, half = e >> 2;
+    __syncthreads();  // every product of this CTA is done: its accumulators have been read
+    if (e >= 0 && e < L::kEpiOn) {
+#pragma unroll
+      for (int j = 0; j < L::kEpiCols; ++j) part[(half * L::kEpiCols + j) * kBM + 32 * q + lane] = acc[j];
+    }
+    cluster.sync();
+    int wt, mt;
+    tile_at(first, n_wt, n_mt, &wt, &mt);
+    pdl_wait();
+    // CTA `rank` adds up and writes tokens rank, rank + S, ...; a warp 32 channels of a token
+    for (int id = warp; id < ((BN - rank + S - 1) / S) * 4; id += kThreads / 32) {
+      const int j = rank + (id >> 2) * S, ch = 32 * (id & 3) + lane;
+      const int m = mt * BN + j, n = wt * kBM + ch;
+      if (m >= M || n >= N || *abort_flag) continue;
+      int32_t sum = 0;
+      for (int r = 0; r < S; ++r) sum += *cluster.map_shared_rank(part + j * kBM + ch, r);
+      const int64_t at = static_cast<int64_t>(m) * N + n;
+      y[at] = round_out<YT>(rescale_elem(static_cast<float>(sum), __frcp_rn(a_scale[m]), __frcp_rn(__ldg(w_scale + n))));
+      if (acc_out) acc_out[at] = sum;
+    }
+    cluster.sync();  // the parts stay until every CTA has read them
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int BN, typename YT>
+cudaError_t launch_bn(const DeviceContext* ctx, EncodeTiledFn encode, const __half* codes, const float* a_scale,
+                      const int8_t* w, const float* w_scale, int M, int N, int K, int S, YT* y, int32_t* acc_out,
+                      bool pdl, cudaStream_t s, int* status) {
+  using L = Layout<BN>;
+  CUtensorMap tm_tok, tm_w;
+  cuuint32_t es[2] = {1, 1};
+  {
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(M)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(K) * 2};
+    cuuint32_t box[2] = {64, static_cast<cuuint32_t>(BN)};
+    if (encode(&tm_tok, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<__half*>(codes), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+      *status = BITNET_ERR_CUDA;
+      return cudaErrorInvalidValue;
+    }
+  }
+  {
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+    cuuint32_t box[2] = {128, static_cast<cuuint32_t>(kBM)};
+    if (encode(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(w), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+      *status = BITNET_ERR_CUDA;
+      return cudaErrorInvalidValue;
+    }
+  }
+  auto kern = k_w8a8_tc<BN, YT>;
+  cudaError_t e = allow_smem(ctx, reinterpret_cast<const void*>(kern), L::kAlloc);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>((N + kBM - 1) / kBM) * ((M + BN - 1) / BN);
+  if (tiles * S > 0x7fffffff) {
+    *status = BITNET_ERR_UNSUPPORTED_SHAPE;
+    return cudaSuccess;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(S > 1 ? tiles * S : (tiles < ctx->num_sms ? tiles : ctx->num_sms)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kAlloc;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  int na = 0;
+  if (pdl) {
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (S > 1) {
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = static_cast<unsigned>(S);
+    attr[na].val.clusterDim.y = 1;
+    attr[na++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = na;
+  return cudaLaunchKernelEx(&cfg, kern, tm_tok, tm_w, a_scale, w_scale, M, N, K, S, y, acc_out, ctx->err_word);
+}
+
+// Token tile and number of K ranges: the cheapest in cycles of the busiest SM,
+// a K block of 128 taking the larger of its shared-memory (4 BN + 256) and unpack
+// (440) cycles, a tile 1500 and a split's exchange 1500 + 8 BN.
+struct Plan {
+  int bn, S;
+};
+Plan make_plan(const DeviceContext* ctx, int64_t M, int64_t K, int64_t N) {
+  Plan best = {192, 1};
+  int64_t best_cost = INT64_MAX;
+  const int64_t nkb = K >> 7;
+  for (int bn : {16, 32, 64, 128, 192}) {
+    const int64_t tiles = ((M + bn - 1) / bn) * ((N + kBM - 1) / kBM);
+    for (int S : {1, 2, 4, 8}) {
+      if (S > nkb || (S > 1 && tiles * S > ctx->num_sms)) continue;  // a split takes one wave
+      const int64_t rounds = (tiles * S + ctx->num_sms - 1) / ctx->num_sms;
+      const int64_t per_kb = 4 * bn + 256 > 440 ? 4 * bn + 256 : 440;
+      const int64_t cost = rounds * (((nkb + S - 1) / S) * per_kb + 1500 + (S > 1 ? 1500 + 8 * bn : 0));
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = {bn, S};
+      }
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
+cudaError_t launch_w8a8_tc(const DeviceContext* ctx, const __half* codes, const float* a_scale, const int8_t* w,
+                           const float* w_scale, int64_t M, int64_t K, int64_t N, void* y, int y_dtype,
+                           int32_t* acc_out, bool pdl, cudaStream_t s, int* status) {
+  *status = BITNET_OK;
+  EncodeTiledFn encode = encode_tiled_fn();
+  if (!encode) {
+    *status = BITNET_ERR_CUDA;
+    return cudaErrorNotSupported;
+  }
+  const Plan pl = make_plan(ctx, M, K, N);
+  const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
+  auto go = [&](auto* yt) {
+    using YT = std::remove_pointer_t<decltype(yt)>;
+    auto f = pl.bn == 16    ? launch_bn<16, YT>
+             : pl.bn == 32  ? launch_bn<32, YT>
+             : pl.bn == 64  ? launch_bn<64, YT>
+             : pl.bn == 128 ? launch_bn<128, YT>
+                            : launch_bn<192, YT>;
+    return f(ctx, encode, codes, a_scale, w, w_scale, m, n, k, pl.S, yt, acc_out, pdl, s, status);
+  };
+  switch (y_dtype) {
+    case BITNET_DTYPE_F32: return go(static_cast<float*>(y));
+    case BITNET_DTYPE_F16: return go(static_cast<__half*>(y));
+    case BITNET_DTYPE_BF16: return go(static_cast<__nv_bfloat16*>(y));
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace bitnet
