@@ -11,16 +11,20 @@
 // tensor memory: 4 warps turn a tile's int8 rows into fp16 straight into TMEM
 // columns (a lane is a channel), so the operand costs shared memory only its
 // int8 bytes, once in and once out.  The tokens' fp16 codes are the N side, BN
-// of them per tile, in shared memory by TMA.  Per 64 of K a tile moves 256 BN +
-// 16384 bytes of shared memory against 2 BN cycles of MMA: shared memory (128
-// bytes a cycle) is the bound from BN = 64 on, at 3/4 of the MMA rate for BN =
-// 192, and the weight stream for few tokens.
+// of them per tile, in shared memory by TMA.
+// Per 64 of K a tile moves 256 BN + 16384 bytes of shared memory against 2 BN
+// cycles of MMA.
 //
-//   warps 0-3   unpack: lane quadrant q, one weight row a thread
-//   warps 4-11  epilogue: quadrant warp & 3, half of the tile's tokens each
-//   warp 12     TMA of raw weights (128 rows x 128 bytes, 128B swizzle)
-//   warp 13     TMA of token codes (64 of K per stage)
-//   warp 14     TMEM, MMA issue
+// A stage is 128 of K (a raw slot): the issuing thread pays some 240 cycles for a
+// wait behind MMAs in flight and 45 per instruction, so it waits once per 8 MMAs
+// (stages of 64 and two waits: 740 cycles per 64 of K whatever BN).  Narrow
+// tiles, whose MMAs are short, run two pipelines (unpack warps, issuer,
+// accumulators), every other stage each.
+//   4 unpack warps per pipeline: lane quadrant q, one weight row a thread; they
+//               also wait for the stage's tokens, so that the issuer has one wait
+//   8 epilogue warps: quadrant, half of the tile's tokens each
+//   a warp for the TMA of raw weights (128 rows x 128 bytes, 128B swizzle), one
+//   for the token codes', and an issuer per pipeline
 // Few tiles (short or narrow problems): a cluster of S CTAs takes a tile, each a
 // range of K, and adds the parts up through distributed shared memory (int32:
 // the order does not matter).
@@ -39,11 +43,9 @@ namespace {
 
 constexpr int kBM = 128;            // channels per tile
 constexpr int kRawBytes = kBM * 128;  // a raw slot: 128 rows x 128 of K
-constexpr int kAStageCols = 32;     // TMEM columns of 64 fp16 of K
+constexpr int kAStageCols = 64;     // TMEM columns of 128 fp16 of K
 constexpr int kChunk = 8;           // K blocks of 128 per exact accumulation
-constexpr int kUnpackWarps = 4, kEpiWarps = 8;
-constexpr int kRawWarp = kUnpackWarps + kEpiWarps, kTokWarp = kRawWarp + 1, kMmaWarp = kRawWarp + 2;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kEpiWarps = 8;
 constexpr int kTmemCols = 512;
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, fp16 operands: A's column c holds K elements 2c, 2c + 1.
@@ -58,22 +60,26 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, 
 
 template <int BN>
 struct Layout {
-  static constexpr int kTokStage = BN * 128;           // 64 of K
-  static constexpr int kTok = BN == 192 ? 6 : 8;
-  static constexpr int kRaw = BN <= 64 ? 9 : (BN == 128 ? 5 : 4);
-  static constexpr int kAStages = BN == 192 ? 4 : 8;   // TMEM: 2 BN accumulator columns, then these
-  static constexpr int kACol0 = 2 * BN;
+  static constexpr int kPipes = BN <= 64 ? 2 : 1;
+  static constexpr int kUnpackWarps = 4 * kPipes;
+  static constexpr int kRawWarp = kUnpackWarps + kEpiWarps, kTokWarp = kRawWarp + 1, kMmaWarp0 = kRawWarp + 2;
+  static constexpr int kThreads = 32 * (kMmaWarp0 + kPipes);
+  static constexpr int kTokStage = BN * 256;           // 128 of K: two 64-wide swizzled slabs
+  static constexpr int kTok = BN == 192 ? 3 : (BN == 128 ? 4 : (BN == 64 ? 5 : 8));
+  static constexpr int kRaw = BN == 192 ? 4 : (BN == 128 ? 5 : 8);
+  static constexpr int kACol0 = 2 * kPipes * BN;       // accumulators [pipe][2], then the A stages
+  static constexpr int kAPer = (kTmemCols - kACol0) / kAStageCols / kPipes;  // A stages of a pipeline
   static constexpr int kEpiCols = BN >= 32 ? BN / 2 : 16;  // token columns per epilogue warp
   static constexpr int kEpiOn = 4 * (BN / kEpiCols);       // epilogue warps with columns
   static constexpr int offTok = 0;
   static constexpr int offRaw = offTok + kTok * kTokStage;
-  static constexpr int kNumBars = 2 * kTok + 2 * kRaw + 2 * kAStages + 4;
+  static constexpr int kNumBars = 2 * kTok + 2 * kRaw + 2 * kPipes * kAPer + 4 * kPipes;
   static constexpr int offBar = offRaw + kRaw * kRawBytes;
   static constexpr int offMisc = offBar + kNumBars * 8;
   static constexpr int kBytes = offMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAPer >= 2, "TMEM columns");
   static_assert(kAlloc <= 232448, "over the 227 KB of shared memory a CTA may use");
-  static_assert(kACol0 + kAStages * kAStageCols <= kTmemCols, "TMEM columns");
   static_assert(kTok * kTokStage + kRaw * kRawBytes >= BN * kBM * 4, "the split's exchange reuses the rings");
 };
 
@@ -89,21 +95,22 @@ __device__ __forceinline__ void tile_at(int t, int n_wt, int n_mt, int* wt, int*
 }
 
 template <int BN, typename YT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Layout<BN>::kThreads, 1)
     k_w8a8_tc(const __grid_constant__ CUtensorMap tm_tok, const __grid_constant__ CUtensorMap tm_w,
               const float* __restrict__ a_scale, const float* __restrict__ w_scale, int M, int N, int K, int S,
               YT* __restrict__ y, int32_t* __restrict__ acc_out, unsigned* err) {
   using L = Layout<BN>;
+  constexpr int kP = L::kPipes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
   uint64_t* tok_full = reinterpret_cast<uint64_t*>(smem + L::offBar);
   uint64_t* tok_empty = tok_full + L::kTok;
   uint64_t* raw_full = tok_empty + L::kTok;
   uint64_t* raw_empty = raw_full + L::kRaw;
-  uint64_t* a_full = raw_empty + L::kRaw;
-  uint64_t* a_empty = a_full + L::kAStages;
-  uint64_t* acc_full = a_empty + L::kAStages;  // [2]
-  uint64_t* acc_empty = acc_full + 2;          // [2]
+  uint64_t* a_full = raw_empty + L::kRaw;           // [pipe][stage]
+  uint64_t* a_empty = a_full + kP * L::kAPer;
+  uint64_t* acc_full = a_empty + kP * L::kAPer;     // [pipe][2]
+  uint64_t* acc_empty = acc_full + 2 * kP;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::offMisc + 4);
 
@@ -123,20 +130,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < L::kRaw; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], kUnpackWarps);
+      mbar_init(&raw_empty[i], 4);
     }
-    for (int i = 0; i < L::kAStages; ++i) {
-      mbar_init(&a_full[i], kUnpackWarps);
+    for (int i = 0; i < kP * L::kAPer; ++i) {
+      mbar_init(&a_full[i], 4);
       mbar_init(&a_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * kP; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], L::kEpiOn);
     }
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == L::kMmaWarp0) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
@@ -147,7 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   int32_t acc[L::kEpiCols];  // epilogue: this thread's channel, its warp's tokens
 
-  if (warp == kRawWarp) {
+  // Block kb of a tile is running number g0 + kb (raw and token rings); pipeline j takes the tile's blocks j, j + kP, ..
+  if (warp == L::kRawWarp) {
     // ------------------------------------------------------------ raw weights
     // (not written by the launch before this one: no wait for it)
     if (lane == 0) {
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*abort_flag)  // given up: copies in flight must land before the CTA's shared memory goes
         for (int k = max(0, i - L::kRaw); k < i; ++k) mbar_wait(&raw_full[k % L::kRaw], (k / L::kRaw) & 1, err);
     }
-  } else if (warp == kTokWarp) {
+  } else if (warp == L::kTokWarp) {
     // ------------------------------------------------------------ token codes
     if (lane == 0) {
       pdl_wait();
@@ -174,67 +182,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = first; t < tiles; t += step) {
         int wt, mt;
         tile_at(t, n_wt, n_mt, &wt, &mt);
-        for (int h = 0; h < 2 * blocks; ++h, ++i) {
+        for (int kb = kb0; kb < kb1; ++kb, ++i) {
           const int s = i % L::kTok;
           if (!mbar_wait(&tok_empty[s], ((i / L::kTok) & 1) ^ 1, err, abort_flag)) goto tok_done;
           mbar_arrive_expect_tx(&tok_full[s], L::kTokStage);
-          tma_load_2d(smem + L::offTok + s * L::kTokStage, &tm_tok, kb0 * 128 + h * 64, mt * BN, &tok_full[s]);
+          uint8_t* dst = smem + L::offTok + s * L::kTokStage;
+          tma_load_2d(dst, &tm_tok, kb * 128, mt * BN, &tok_full[s]);
+          tma_load_2d(dst + BN * 128, &tm_tok, kb * 128 + 64, mt * BN, &tok_full[s]);
         }
       }
     tok_done:
       if (*abort_flag)
         for (int k = max(0, i - L::kTok); k < i; ++k) mbar_wait(&tok_full[k % L::kTok], (k / L::kTok) & 1, err);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= L::kMmaWarp0) {
     // ------------------------------------------------------------ MMA issue
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_f16_f32(kBM, BN);
-      int i = 0, c = 0;  // running stages and chunks
-      for (int t = first; t < tiles; t += step) {
-        for (int h0 = 0; h0 < 2 * blocks; h0 += 2 * kChunk, ++c) {
-          if (!mbar_wait(&acc_empty[c & 1], ((c >> 1) & 1) ^ 1, err, abort_flag)) goto mma_done;
-          tc_fence_after();
-          const uint32_t d = tmem + static_cast<uint32_t>((c & 1) * BN);
-          const int h1 = min(h0 + 2 * kChunk, 2 * blocks);
-          for (int h = h0; h < h1; ++h, ++i) {
-            const int s = i % L::kTok, as = i % L::kAStages;
-            if (!mbar_wait(&tok_full[s], (i / L::kTok) & 1, err, abort_flag)) goto mma_done;
-            if (!mbar_wait(&a_full[as], (i / L::kAStages) & 1, err, abort_flag)) goto mma_done;
+      const int j = warp - L::kMmaWarp0;
+      int n = 0, c = 0, g0 = 0;  // running stages and chunks of the pipeline, blocks of the CTA
+      for (int t = first; t < tiles; t += step, g0 += blocks) {
+        for (int kb = j, in = 0; kb < blocks; kb += kP, ++n) {
+          const uint32_t d = tmem + static_cast<uint32_t>((2 * j + (c & 1)) * BN);
+          if (in == 0) {
+            if (!mbar_wait(&acc_empty[2 * j + (c & 1)], ((c >> 1) & 1) ^ 1, err, abort_flag)) goto mma_done;
             tc_fence_after();
-            const uint64_t bd = sw128_kmajor_desc(smem_u32(smem + L::offTok + s * L::kTokStage));
-            const uint32_t at = tmem + static_cast<uint32_t>(L::kACol0 + as * kAStageCols);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma_f16_ta(d, at + 8 * k, bd + 2 * k, idesc, (h > h0 || k) ? 1u : 0u);
-            tc_commit(&tok_empty[s]);
-            tc_commit(&a_empty[as]);
           }
-          tc_commit(&acc_full[c & 1]);
+          const int as = L::kAPer * j + n % L::kAPer, s = (g0 + kb) % L::kTok;
+          if (!mbar_wait(&a_full[as], (n / L::kAPer) & 1, err, abort_flag)) goto mma_done;  // the tokens, too
+          tc_fence_after();
+          const uint64_t bd = sw128_kmajor_desc(smem_u32(smem + L::offTok + s * L::kTokStage));
+          const uint32_t at = tmem + static_cast<uint32_t>(L::kACol0 + as * kAStageCols);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_f16_ta(d, at + 8 * k, bd + (k >> 2) * (BN * 128 / 16) + 2 * (k & 3), idesc, (in || k) ? 1u : 0u);
+          tc_commit(&a_empty[as]);
+          tc_commit(&tok_empty[s]);
+          if (++in == kChunk || kb + kP >= blocks) {
+            tc_commit(&acc_full[2 * j + (c & 1)]);
+            ++c;
+            in = 0;
+          }
         }
       }
     mma_done:
       if (*abort_flag) {  // the products in flight must end before shared and tensor memory go
-        // a barrier of its own use: the chunk barriers' phases are unknown here
-        uint64_t* drained = reinterpret_cast<uint64_t*>(smem + L::offMisc + 16);
+        // a barrier of its own use: the others' phases are unknown here
+        uint64_t* drained = reinterpret_cast<uint64_t*>(smem + L::offMisc + 16) + j;
         mbar_init(drained, 1);
         fence_barrier_init();
         tc_commit(drained);
         mbar_wait(drained, 0, err);
       }
     }
-  } else if (warp < kUnpackWarps) {
+  } else if (warp < L::kUnpackWarps) {
     // ------------------------------------------------------------ unpack
-    const int row = 32 * warp + lane;
-    const uint32_t tq = tmem + (static_cast<uint32_t>(32 * warp) << 16) + static_cast<uint32_t>(L::kACol0);
-    int i = 0, r = 0;  // running stages and raw slots
-    bool pending = false;  // a stage's stores are under way and not yet announced
-    for (int t = first; t < tiles; t += step) {
-      for (int kb = 0; kb < blocks; ++kb, ++r) {
-        const int rs = r % L::kRaw;
-        if (!mbar_wait(&raw_full[rs], (r / L::kRaw) & 1, err, abort_flag)) goto unpack_done;
+    const int j = warp >> 2, q = warp & 3, row = 32 * q + lane;
+    const uint32_t tq = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(L::kACol0);
+    int n = 0, g0 = 0;
+    int pending = -1;  // running block whose stores are under way and not yet announced
+    auto announce = [&]() {
+      tmem_st_wait();
+      tc_fence_before();
+      const bool ok = mbar_wait(&tok_full[pending % L::kTok], (pending / L::kTok) & 1, err, abort_flag);
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&a_full[L::kAPer * j + (n - 1) % L::kAPer]);
+      pending = -1;
+      return ok;
+    };
+    for (int t = first; t < tiles; t += step, g0 += blocks) {
+      for (int kb = j; kb < blocks; kb += kP) {
+        const int g = g0 + kb, rs = g % L::kRaw;
+        if (pending >= 0 && !mbar_test(&raw_full[rs], (g / L::kRaw) & 1) && !announce()) goto unpack_done;
+        if (!mbar_wait(&raw_full[rs], (g / L::kRaw) & 1, err, abort_flag)) goto unpack_done;
         const uint8_t* src = smem + L::offRaw + rs * kRawBytes + row * 128;
+        const int as = L::kAPer * j + n % L::kAPer;
 #pragma unroll
-        for (int h = 0; h < 2; ++h, ++i) {
+        for (int h = 0; h < 2; ++h) {
           uint32_t cols[32];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -244,66 +268,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             int8_to_h2(v.z, cols[8 * c + 4], cols[8 * c + 5]);
             int8_to_h2(v.w, cols[8 * c + 6], cols[8 * c + 7]);
           }
-          if (h == 1) {  // the slot's bytes are in registers
+          if (h == 0) {
+            // announce the stage before, whose stores ran during this decode
+            if (pending >= 0 && !announce()) goto unpack_done;
+            if (!mbar_wait(&a_empty[as], ((n / L::kAPer) & 1) ^ 1, err, abort_flag)) goto unpack_done;
+            tc_fence_after();
+          } else {  // the slot's bytes are in registers
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&raw_empty[rs]);
           }
-          // announce the stage before, whose stores ran during this decode
-          if (pending) {
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&a_full[(i - 1) % L::kAStages]);
-          }
-          const int as = i % L::kAStages;
-          if (!mbar_wait(&a_empty[as], ((i / L::kAStages) & 1) ^ 1, err, abort_flag)) goto unpack_done;
-          tc_fence_after();
           __syncwarp();
-          tmem_st_32x32b_x32(tq + static_cast<uint32_t>(as * kAStageCols), cols);
-          pending = true;
+          tmem_st_32x32b_x32(tq + static_cast<uint32_t>(as * kAStageCols + 32 * h), cols);
         }
+        pending = g;
+        ++n;
       }
     }
-    if (pending) {
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&a_full[(i - 1) % L::kAStages]);
-    }
+    if (pending >= 0) announce();
   unpack_done:;
   } else {
     // ------------------------------------------------------------ epilogue
-    const int e = warp - kUnpackWarps, q = warp & 3, half = e >> 2;
+    const int e = warp - L::kUnpackWarps, q = warp & 3, half = e >> 2;
     if (e < L::kEpiOn) {
       pdl_wait();  // the tokens' scales
       const uint32_t tq = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(half * L::kEpiCols);
-      int c = 0;
+      int c[kP] = {};  // running chunks of each pipeline
       for (int t = first; t < tiles; t += step) {
         int wt, mt;
         tile_at(t, n_wt, n_mt, &wt, &mt);
         bool ok = true;
-        for (int h0 = 0; h0 < blocks; h0 += kChunk, ++c) {
-          if (!mbar_wait_idle(&acc_full[c & 1], (c >> 1) & 1, err, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
 #pragma unroll
-          for (int j = 0; j < L::kEpiCols; j += 16) {
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(tq + static_cast<uint32_t>((c & 1) * BN + j), v);
-            tmem_ld_wait();
-            tmem_reg_fence16(v);
+        for (int k = 0; k < L::kEpiCols; ++k) acc[k] = 0;
+        for (int h0 = 0; ok && h0 < blocks; h0 += kP * kChunk) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int d = __float2int_rn(__uint_as_float(v[k]));
-              acc[j + k] = h0 == 0 ? d : acc[j + k] + d;
+          for (int j = 0; j < kP; ++j) {
+            if (h0 + j >= blocks) break;  // no block of this chunk is the pipeline's
+            const int buf = 2 * j + (c[j] & 1);
+            if (!mbar_wait_idle(&acc_full[buf], (c[j] >> 1) & 1, err, abort_flag)) {
+              ok = false;
+              break;
             }
+            tc_fence_after();
+#pragma unroll
+            for (int k0 = 0; k0 < L::kEpiCols; k0 += 16) {
+              uint32_t v[16];
+              tmem_ld_32x32b_x16(tq + static_cast<uint32_t>(buf * BN + k0), v);
+              tmem_ld_wait();
+              tmem_reg_fence16(v);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) acc[k0 + k] += __float2int_rn(__uint_as_float(v[k]));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            ++c[j];
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[c & 1]);
         }
         if (!ok) break;
         if (S > 1) break;  // one tile; the parts meet below
@@ -334,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     int32_t* part = reinterpret_cast<int32_t*>(smem);
-    const int e = warp - kUnpackWarps, q = warp & 3, half = e >> 2;
+    const int e = warp - L::kUnpackWarps, q = warp & 3, half = e >> 2;
     __syncthreads();  // every product of this CTA is done: its accumulators have been read
     if (e >= 0 && e < L::kEpiOn) {
 #pragma unroll
@@ -345,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tile_at(first, n_wt, n_mt, &wt, &mt);
     pdl_wait();
     // CTA `rank` adds up and writes tokens rank, rank + S, ...; a warp 32 channels of a token
-    for (int id = warp; id < ((BN - rank + S - 1) / S) * 4; id += kThreads / 32) {
+    for (int id = warp; id < ((BN - rank + S - 1) / S) * 4; id += L::kThreads / 32) {
       const int j = rank + (id >> 2) * S, ch = 32 * (id & 3) + lane;
       const int m = mt * BN + j, n = wt * kBM + ch;
       if (m >= M || n >= N || *abort_flag) continue;
@@ -359,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == L::kMmaWarp0) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -404,7 +424,7 @@ cudaError_t launch_bn(const DeviceContext* ctx, EncodeTiledFn encode, const __ha
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(S > 1 ? tiles * S : (tiles < ctx->num_sms ? tiles : ctx->num_sms)));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kAlloc;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -425,8 +445,9 @@ cudaError_t launch_bn(const DeviceContext* ctx, EncodeTiledFn encode, const __ha
 }
 
 // Token tile and number of K ranges: the cheapest in cycles of the busiest SM,
-// a K block of 128 taking the larger of its shared-memory (4 BN + 256) and unpack
-// (440) cycles, a tile 1500 and a split's exchange 1500 + 8 BN.
+// a K block of 128 taking the larger of its shared-memory (4 BN + 256) and its
+// pipelines' (740, 380 with two) cycles, a tile 1500 and a split's exchange 1500 +
+// 8 BN.
 struct Plan {
   int bn, S;
 };
@@ -439,7 +460,8 @@ Plan make_plan(const DeviceContext* ctx, int64_t M, int64_t K, int64_t N) {
     for (int S : {1, 2, 4, 8}) {
       if (S > nkb || (S > 1 && tiles * S > ctx->num_sms)) continue;  // a split takes one wave
       const int64_t rounds = (tiles * S + ctx->num_sms - 1) / ctx->num_sms;
-      const int64_t per_kb = 4 * bn + 256 > 440 ? 4 * bn + 256 : 440;
+      const int64_t pipes = bn <= 64 ? 380 : 740;
+      const int64_t per_kb = 4 * bn + 256 > pipes ? 4 * bn + 256 : pipes;
       const int64_t cost = rounds * (((nkb + S - 1) / S) * per_kb + 1500 + (S > 1 ? 1500 + 8 * bn : 0));
       if (cost < best_cost) {
         best_cost = cost;
