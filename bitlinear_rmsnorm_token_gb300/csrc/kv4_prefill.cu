@@ -34,7 +34,6 @@ namespace bitnet {
 namespace {
 
 constexpr int kRows = 128;          // rows of a tile
-constexpr int kUnpackWarps = 4;
 constexpr float kLazy = 8.0f;       // a row's maximum may pass its reference by this many powers of two
 constexpr int kWExp = 6;            // value scales are below 2^(kWExp + 1) after their power of two: times 2^kLazy < 2^15
 
@@ -50,6 +49,32 @@ __device__ __forceinline__ int pow2_exp(float v) { return min(max((__float_as_in
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Pairs of floats in one 64-bit register: two operations an instruction.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_pack(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(f2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Codes in bits 0-3 (4-7) of both halves of w, other bits ignored, to fp16 c - 8.
@@ -85,8 +110,8 @@ __device__ __forceinline__ void tmem_ld_32x32b_x4(uint32_t taddr, uint32_t* r) {
 
 // A page's per-key factors, and what the softmax has to know of the page.
 struct __align__(16) PageMeta {
-  float2 k[kKvPage];  // s, m + 8 s of the keys
-  float2 v[kKvPage];  // s 2^(kWExp - e), m + 8 s of the values
+  float ks[kKvPage], kmid[kKvPage];  // s, m + 8 s of the keys
+  float vs[kKvPage], vmid[kKvPage];  // s 2^(kWExp - e), m + 8 s of the values
   int key0;           // position of the page's first token
   int ok;             // 0: no such page, its keys are masked
   int grow;           // e has grown by this much since the page before
@@ -98,8 +123,9 @@ struct Layout {
   static constexpr int kT = D == 128 ? 2 : 1;                // tiles per CTA
   static constexpr int kParts = kSplit ? 2 : 1;
   static constexpr int kRaw = D == 256 && kSplit ? 1 : 2;    // raw page slots
-  static constexpr int kK = D == 256 && kSplit ? 1 : 2;      // key operand stages
-  static constexpr int kV = D == 256 ? 1 : 2;                // value operand stages
+  static constexpr int kK = D == 256 ? 1 : 2;                // key operand stages
+  static constexpr int kV = D == 256 && kSplit ? 1 : 2;      // value operand stages
+  static constexpr int kUnpackWarps = D == 256 ? 8 : 4;
   static constexpr int kMeta = 4;
   static constexpr int kSoftWarps = 4 * kT;
   static constexpr int kProducer = kSoftWarps + kUnpackWarps;
@@ -114,7 +140,8 @@ struct Layout {
   static constexpr int offMeta = offRaw + kRaw * KvBlock<D>::kBytes;
   static constexpr int kNumBars = 2 * kRaw + 2 * kK + 2 * kV + 2 * kMeta + 5 * kT;
   static constexpr int offBar = offMeta + kMeta * static_cast<int>(sizeof(PageMeta));
-  static constexpr int offMisc = offBar + kNumBars * 8;      // 32 ints
+  static constexpr int offRow = offBar + kNumBars * 8;       // float2 per row: sum(q), its factor
+  static constexpr int offMisc = offRow + kT * kRows * 8;    // 32 ints
   static constexpr int kBytes = offMisc + 128;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 232448, "over the 227 KB of shared memory a CTA may use");
@@ -226,18 +253,18 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kRaw; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], kUnpackWarps);
+      mbar_init(&raw_empty[i], L::kUnpackWarps);
     }
     for (int i = 0; i < L::kK; ++i) {
-      mbar_init(&k_full[i], kUnpackWarps);
+      mbar_init(&k_full[i], L::kUnpackWarps);
       mbar_init(&k_empty[i], kT);
     }
     for (int i = 0; i < L::kV; ++i) {
-      mbar_init(&v_full[i], kUnpackWarps);
+      mbar_init(&v_full[i], L::kUnpackWarps);
       mbar_init(&v_empty[i], kT);
     }
     for (int i = 0; i < L::kMeta; ++i) {
-      mbar_init(&meta_full[i], kUnpackWarps);
+      mbar_init(&meta_full[i], L::kUnpackWarps);
       mbar_init(&meta_empty[i], L::kSoftWarps);
     }
     for (int i = 0; i < kT; ++i) {
@@ -254,58 +281,55 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
     tmem_alloc(tmem_slot, L::kCols);
     tmem_relinquish();
   }
-  // ---- queries: a softmax thread's row, scaled by a power of two, as fp16 (one part or two)
-  float qsum = 0.0f, qc = 0.0f;
-  const int tile = warp >> 2;                               // softmax warps
-  const int r = row0 + tile * kRows + (threadIdx.x & 127);  // row of the item
-  const bool row_on = warp < L::kSoftWarps && r < rows;
-  const int i_tok = row_on ? r / p.G : 0;
-  const int64_t q_at = (static_cast<int64_t>(q0 + i_tok) * p.Hq + head * p.G + (row_on ? r - i_tok * p.G : 0));
-  if (warp < L::kSoftWarps) {
-    const QT* src = q + q_at * D;
-    float top = 0.0f;
-    if (row_on) {
-#pragma unroll 8
-      for (int i = 0; i < D / 4; ++i) {
-        const float4 v = load4(src + 4 * i);
-        top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
-      }
-    }
-    const int e = pow2_exp(top);
-    const float f = p.sign * pow2(14 - e);
-    qc = p.scale * pow2(e - 14);
-    const int rr = threadIdx.x & 127;
-#pragma unroll 2
-    for (int c = 0; c < D / 8; ++c) {
+  // ---- queries, scaled by a power of two per row, as fp16 (one part or two): D / 8 lanes to a row, 8 dimensions each
+  float2* row_q = reinterpret_cast<float2*>(smem + L::offRow);
+  {
+    constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes of a row, rows of a warp at a time
+    constexpr int kStep = L::kThreads / 32 * kAt;
+    const int c = lane % kLanes;
+#pragma unroll 4
+    for (int rr = warp * kAt + lane / kLanes; rr < kT * kRows; rr += kStep) {
+      const int row = row0 + rr;
+      const bool on = row < rows;
+      const int i = on ? row / p.G : 0;
+      const QT* src = q + (static_cast<int64_t>(q0 + i) * p.Hq + head * p.G + (on ? row - i * p.G : 0)) * D + 8 * c;
       float v[8];
+      const float4 a = on ? load4(src) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const float4 b4 = on ? load4(src + 4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b4.x; v[5] = b4.y; v[6] = b4.z; v[7] = b4.w;
+      float top = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 u = row_on ? load4(src + 8 * c + 4 * i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        v[4 * i] = u.x * f;
-        v[4 * i + 1] = u.y * f;
-        v[4 * i + 2] = u.z * f;
-        v[4 * i + 3] = u.w * f;
-      }
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]));
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = pow2_exp(top);
+      const float f = p.sign * pow2(14 - e);
       // chunk c of the row: dimensions 8c + 0, 4, 1, 5, 2, 6, 3, 7, the order in which a word of codes decodes
-      uint8_t* dst = smem + L::offQ + tile * L::kParts * L::kQPart + (c >> 3) * (kRows * 128) + (rr >> 3) * 1024 +
-                     (rr & 7) * 128 + (((c & 7) ^ (rr & 7)) << 4);
-      float h[8];
+      const int tl = rr / kRows, rt = rr % kRows;
+      uint8_t* dst = smem + L::offQ + tl * L::kParts * L::kQPart + (c >> 3) * (kRows * 128) + (rt >> 3) * 1024 +
+                     (rt & 7) * 128 + (((c & 7) ^ (rt & 7)) << 4);
+      float h[8], sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        h[i] = __half2float(__float2half_rn(v[i]));
-        qsum += h[i];
+      for (int k = 0; k < 8; ++k) {
+        v[k] *= f;
+        h[k] = __half2float(__float2half_rn(v[k]));
+        sum += h[k];
       }
       *reinterpret_cast<uint4*>(dst) =
           make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
       if constexpr (kSplit) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          h[i] = __half2float(__float2half_rn(v[i] - h[i]));
-          qsum += h[i];
+        for (int k = 0; k < 8; ++k) {
+          h[k] = __half2float(__float2half_rn(v[k] - h[k]));
+          sum += h[k];
         }
         *reinterpret_cast<uint4*>(dst + L::kQPart) =
             make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
       }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (c == 0) row_q[rr] = make_float2(sum, p.scale * pow2(e - 14));
     }
     fence_proxy_async_smem();
   }
@@ -317,16 +341,135 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
   if (warp < L::kSoftWarps) {
     // ------------------------------------------------------------ softmax
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;  // this warp's quarter of the TMEM lanes
+    const int tile = warp >> 2;
+    const int tile_r0 = row0 + tile * kRows;
+    const int r = tile_r0 + (threadIdx.x & 127);  // row of the item
+    const bool row_on = r < rows;
+    const int i_tok = row_on ? r / p.G : 0;
+    const int64_t q_at = static_cast<int64_t>(q0 + i_tok) * p.Hq + head * p.G + (row_on ? r - i_tok * p.G : 0);
+    const float2 row = row_q[threadIdx.x];
+    const float qc = row.y;
+    const f2 qsum2 = f2_pack(row.x, row.x), qc2 = f2_pack(qc, qc);
     const int pos = row_on ? pos0 + i_tok : len - 1;
     const int key_hi = p.causal ? min(pos, len - 1) : len - 1;
     const int key_lo = p.causal && p.window > 0 ? pos - p.window + 1 : 0;
     // pages between these need no mask for any row of the tile
-    const int tile_r0 = row0 + tile * kRows;
     const int free_hi = p.causal ? min(pos0 + tile_r0 / p.G, len - 1) : len - 1;
     const int free_lo = p.causal && p.window > 0 ? pos0 + (min(tile_r0 + kRows, rows) - 1) / p.G - p.window + 1 : 0;
-    float m_ref = -INFINITY, l = 0.0f, z = 0.0f;
+    float m_ref = -INFINITY;
+    f2 l2 = 0, z2 = 0;  // sums of the even and of the odd keys
     int e_run = 0;
     bool ok = true;
+    // A page's share of the softmax; kMasked: some key of it is hidden from some row of the tile.
+    auto page = [&](int j, uint32_t s_addr, const PageMeta& meta, auto masked_tag) -> bool {
+      constexpr bool kMasked = decltype(masked_tag)::value;
+      f2 x[32];
+      float top = -INFINITY;
+      {
+        uint32_t s0[32], s1[32];
+        tmem_ld_32x32b_x32(s_addr, s0);
+        tmem_ld_32x32b_x32(s_addr + 32, s1);
+        tmem_ld_wait();
+        tmem_reg_fence(s0);
+        tmem_reg_fence(s1);
+        [[maybe_unused]] const int hi = meta.ok ? key_hi - meta.key0 : -1, lo = key_lo - meta.key0;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(&meta.ks[2 * i]);
+          const ulonglong2 km = *reinterpret_cast<const ulonglong2*>(&meta.kmid[2 * i]);
+          const uint32_t* sv = i < 16 ? s0 + 2 * i : s1 + 2 * i - 32;
+          x[i] = f2_fma(f2_pack(__uint_as_float(sv[0]), __uint_as_float(sv[1])), ks.x, f2_mul(km.x, qsum2));
+          x[i + 1] = f2_fma(f2_pack(__uint_as_float(sv[2]), __uint_as_float(sv[3])), ks.y, f2_mul(km.y, qsum2));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float a, b;
+            f2_unpack(x[i + k], a, b);
+            if constexpr (kMasked) {
+              const int key = 2 * (i + k);
+              if (key > hi || key < lo) a = -INFINITY;
+              if (key + 1 > hi || key + 1 < lo) b = -INFINITY;
+              x[i + k] = f2_pack(a, b);
+            }
+            top = fmaxf(top, fmaxf(a, b));
+          }
+        }
+      }
+      // ---- the reference, and O with it where it moves
+      float f = 1.0f;
+      if (top != -INFINITY) {
+        const float m = top * qc;
+        if (m_ref == -INFINITY) {
+          m_ref = m;  // nothing summed yet
+        } else if (m > m_ref + kLazy) {
+          f = ex2(m_ref - m);
+          m_ref = m;
+          const f2 ff = f2_pack(f, f);
+          l2 = f2_mul(l2, ff);
+          z2 = f2_mul(z2, ff);
+        }
+      }
+      if (meta.grow) f *= pow2(-meta.grow);
+      if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+        if (!mbar_wait(&pv_done[tile], (j - 1) & 1, p.err, abort_flag)) return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16];
+          tmem_ld_32x32b_x16(tmem + lanes + static_cast<uint32_t>(L::o_col(tile) + c), o);
+          tmem_ld_wait();
+          tmem_reg_fence16(o);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+          tmem_st_32x32b_x16(tmem + lanes + static_cast<uint32_t>(L::o_col(tile) + c), o);
+        }
+        tmem_st_wait();
+      }
+      // ---- probabilities, sums, and W over the scores, 32 keys at a time
+      const float ref = m_ref == -INFINITY ? 0.0f : -m_ref;
+      const f2 ref2 = f2_pack(ref, ref);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t w0[16];
+        [[maybe_unused]] uint32_t w1[16];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const ulonglong2 vs = *reinterpret_cast<const ulonglong2*>(&meta.vs[32 * hf + 2 * i]);
+          const ulonglong2 vm = *reinterpret_cast<const ulonglong2*>(&meta.vmid[32 * hf + 2 * i]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const f2 xi = x[16 * hf + i + k];
+            float a, b, wa, wb;
+            f2_unpack(f2_fma(xi, qc2, ref2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            f2 pr = f2_pack(a, b), w = f2_mul(pr, k ? vs.y : vs.x), zi = f2_mul(pr, k ? vm.y : vm.x);
+            if constexpr (kMasked) {  // whatever the value row of a masked key holds
+              float xa, xb, za, zb;
+              f2_unpack(xi, xa, xb);
+              f2_unpack(w, wa, wb);
+              f2_unpack(zi, za, zb);
+              if (xa == -INFINITY) a = wa = za = 0.0f;
+              if (xb == -INFINITY) b = wb = zb = 0.0f;
+              pr = f2_pack(a, b);
+              w = f2_pack(wa, wb);
+              zi = f2_pack(za, zb);
+            }
+            l2 = f2_add(l2, pr);
+            z2 = f2_add(z2, zi);
+            f2_unpack(w, wa, wb);
+            w0[i + k] = pack_h2(wa, wb);
+            if constexpr (kSplit) {
+              const __half2 h = *reinterpret_cast<const __half2*>(&w0[i + k]);
+              w1[i + k] = pack_h2(wa - __low2float(h), wb - __high2float(h));
+            }
+          }
+        }
+        tmem_st_32x32b_x16(s_addr + 16 * hf, w0);
+        if constexpr (kSplit) tmem_st_32x32b_x16(s_addr + 32 + 16 * hf, w1);
+      }
+      tmem_st_wait();
+      return true;
+    };
     for (int j = 0; j < pages; ++j) {
       const int buf = j & 1, ms = j % L::kMeta;
       const uint32_t s_addr = tmem + lanes + static_cast<uint32_t>(L::s_col(tile, buf));
@@ -337,92 +480,24 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
       }
       tc_fence_after();
       const PageMeta& meta = metas[ms];
-      const int key0 = meta.key0, grow = meta.grow;
-      const bool masked = !meta.ok || key0 < free_lo || key0 + kKvPage - 1 > free_hi;
       e_run = meta.e;
-      uint32_t s0[32], s1[32];
-      tmem_ld_32x32b_x32(s_addr, s0);
-      tmem_ld_32x32b_x32(s_addr + 32, s1);
-      tmem_ld_wait();
-      tmem_reg_fence(s0);
-      tmem_reg_fence(s1);
-      float x[64];
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 64; i += 2) {
-        const float4 km = *reinterpret_cast<const float4*>(&meta.k[i]);
-        x[i] = fmaf(__uint_as_float(i < 32 ? s0[i & 31] : s1[i & 31]), km.x, km.y * qsum);
-        x[i + 1] = fmaf(__uint_as_float(i < 32 ? s0[(i + 1) & 31] : s1[(i + 1) & 31]), km.z, km.w * qsum);
-      }
-      if (masked) {
-        const int hi = meta.ok ? key_hi - key0 : -1, lo = key_lo - key0;
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (i > hi || i < lo) x[i] = -INFINITY;
-      }
-#pragma unroll
-      for (int i = 0; i < 64; ++i) top = fmaxf(top, x[i]);
-      // ---- the reference, and O with it where it moves
-      float f = 1.0f;
-      if (top != -INFINITY) {
-        const float m = top * qc;
-        if (m_ref == -INFINITY) {
-          m_ref = m;  // nothing summed yet
-        } else if (m > m_ref + kLazy) {
-          f = ex2(m_ref - m);
-          m_ref = m;
-          l *= f;
-          z *= f;
-        }
-      }
-      if (grow) f *= pow2(-grow);
-      if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-        if (!mbar_wait(&pv_done[tile], (j - 1) & 1, p.err, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(tmem + lanes + static_cast<uint32_t>(L::o_col(tile) + c), o);
-          tmem_ld_wait();
-          tmem_reg_fence(o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st_32x32b_x32(tmem + lanes + static_cast<uint32_t>(L::o_col(tile) + c), o);
-        }
-        tmem_st_wait();
-      }
-      // ---- probabilities, sums, and W over the scores
-      const float ref = m_ref == -INFINITY ? 0.0f : m_ref;
-      uint32_t w0[32], w1[32];
-#pragma unroll
-      for (int i = 0; i < 64; i += 2) {
-        const float4 vm = *reinterpret_cast<const float4*>(&meta.v[i]);
-        float pa = ex2(fmaf(x[i], qc, -ref)), pb = ex2(fmaf(x[i + 1], qc, -ref));
-        float wa = pa * vm.x, wb = pb * vm.z, za = pa * vm.y, zb = pb * vm.w;
-        if (masked) {  // whatever the value row of a masked key holds
-          if (x[i] == -INFINITY) pa = wa = za = 0.0f;
-          if (x[i + 1] == -INFINITY) pb = wb = zb = 0.0f;
-        }
-        l += pa + pb;
-        z += za + zb;
-        w0[i >> 1] = pack_h2(wa, wb);
-        if constexpr (kSplit) {
-          const __half2 h = *reinterpret_cast<const __half2*>(&w0[i >> 1]);
-          w1[i >> 1] = pack_h2(wa - __low2float(h), wb - __high2float(h));
-        }
-      }
-      tmem_st_32x32b_x32(s_addr, w0);
-      if constexpr (kSplit) tmem_st_32x32b_x32(s_addr + 32, w1);
-      tmem_st_wait();
+      const bool masked = !meta.ok || meta.key0 < free_lo || meta.key0 + kKvPage - 1 > free_hi;
+      ok = masked ? page(j, s_addr, meta, std::true_type{}) : page(j, s_addr, meta, std::false_type{});
+      if (!ok) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&p_full[tile]);
         mbar_arrive(&meta_empty[ms]);
       }
+    }
+    float l, z;
+    {
+      float a, b;
+      f2_unpack(l2, a, b);
+      l = a + b;
+      f2_unpack(z2, a, b);
+      z = a + b;
     }
     // ---- the row's result
     if (ok && (pages == 0 || mbar_wait(&pv_done[tile], (pages - 1) & 1, p.err, abort_flag))) {
@@ -472,27 +547,40 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
     }
   } else if (warp < L::kProducer) {
     // ------------------------------------------------------------ unpack
-    const int ut = threadIdx.x - 32 * L::kSoftWarps;  // 0 .. 127
+    constexpr int kU = 32 * L::kUnpackWarps;
+    const int ut = threadIdx.x - 32 * L::kSoftWarps;  // 0 .. kU - 1
     constexpr int kWords = D / 8;                     // words of a row
     int e_run = -1000;
     for (int j = 0; j < pages; ++j) {
       const int rs = j % L::kRaw, ks = j % L::kK, vs = j % L::kV, ms = j % L::kMeta;
-      if (!mbar_wait(&raw_full[rs], (j / L::kRaw) & 1, p.err, abort_flag)) break;
-      const uint8_t* raw = smem + L::offRaw + rs * B::kBytes;
       const int page = p.c.page_table[static_cast<int64_t>(b) * p.c.max_pages + page0 + j];
       const bool ok = page >= 0 && page < p.c.num_pages;
-      // ---- keys: a word (8 dimensions) to a 16-byte chunk of the key's operand row
+      if (!mbar_wait(&raw_full[rs], (j / L::kRaw) & 1, p.err, abort_flag)) break;
+      const uint8_t* raw = smem + L::offRaw + rs * B::kBytes;
+      // ---- keys: a word (8 dimensions) to a 16-byte chunk of the key's operand row.  A thread keeps its word column
+      // and goes down the keys in steps that are multiples of 8, which leave the swizzle as it is.
       if (!mbar_wait(&k_empty[ks], ((j / L::kK) & 1) ^ 1, p.err, abort_flag)) break;
-      uint8_t* kop = smem + L::offK + ks * L::kOp;
-#pragma unroll 4
-      for (int i = 0; i < kKvPage * kWords / 128; ++i) {
-        const int id = i * 128 + ut, w = id % kWords, key = id / kWords;
-        const uint32_t a = ok ? *reinterpret_cast<const uint32_t*>(raw + B::offK + key * B::kRow + 4 * w) : 0x88888888u;
-        const uint32_t a8 = a >> 8;
-        *reinterpret_cast<uint4*>(kop + (w >> 3) * (kKvPage * 128) + (key >> 3) * 1024 + (key & 7) * 128 +
-                                  (((w & 7) ^ (key & 7)) << 4)) =
-            make_uint4(codes_lo(a), codes_hi(a), codes_lo(a8), codes_hi(a8));
+      {
+        constexpr int kStep = kU / kWords;  // 8
+        static_assert(kStep % 8 == 0, "the swizzle repeats every 8 rows");
+        const int w = ut % kWords, key = ut / kWords;
+        const uint8_t* src = raw + B::offK + key * B::kRow + 4 * w;
+        uint8_t* dst = smem + L::offK + ks * L::kOp + (w >> 3) * (kKvPage * 128) + (key >> 3) * 1024 + (key & 7) * 128 +
+                       (((w & 7) ^ (key & 7)) << 4);
+        uint32_t a[kKvPage / kStep];
+#pragma unroll
+        for (int i = 0; i < kKvPage / kStep; ++i)
+          a[i] = ok ? *reinterpret_cast<const uint32_t*>(src + i * kStep * B::kRow) : 0x88888888u;
+#pragma unroll
+        for (int i = 0; i < kKvPage / kStep; ++i) {
+          const uint32_t a8 = a[i] >> 8;
+          *reinterpret_cast<uint4*>(dst + i * kStep * 128) =
+              make_uint4(codes_lo(a[i]), codes_hi(a[i]), codes_lo(a8), codes_hi(a8));
+        }
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full[ks]);
       // ---- factors
       if (!mbar_wait(&meta_empty[ms], ((j / L::kMeta) & 1) ^ 1, p.err, abort_flag)) break;
       {
@@ -513,13 +601,14 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
           e_run = e_pg + 1;
         }
         PageMeta& meta = metas[ms];
-        const float f = pow2(kWExp - e_run);
-        const bool is_v = ut >= kKvPage;
-        const int key = ut & (kKvPage - 1);
-        const float2 sm = reinterpret_cast<const float2*>(raw + (is_v ? B::offVMeta : B::offKMeta))[key];
-        const float mid = fmaf(8.0f, sm.x, sm.y);
-        if (is_v) meta.v[key] = make_float2(sm.x * f, mid);
-        else meta.k[key] = make_float2(sm.x, mid);
+        if (ut < 2 * kKvPage) {
+          const bool is_v = ut >= kKvPage;
+          const int key = ut & (kKvPage - 1);
+          const float2 sm = reinterpret_cast<const float2*>(raw + (is_v ? B::offVMeta : B::offKMeta))[key];
+          const float mid = fmaf(8.0f, sm.x, sm.y);
+          (is_v ? meta.vs : meta.ks)[key] = is_v ? sm.x * pow2(kWExp - e_run) : sm.x;
+          (is_v ? meta.vmid : meta.kmid)[key] = mid;
+        }
         if (ut == 0) {
           meta.key0 = key0;
           meta.ok = ok ? 1 : 0;
@@ -527,33 +616,28 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
           meta.e = e_run;
         }
       }
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&k_full[ks]);
-        mbar_arrive(&meta_full[ms]);
-      }
+      if (lane == 0) mbar_arrive(&meta_full[ms]);
       // ---- values, transposed: a word of 8 consecutive keys to 8 chunks, one per dimension; dimension 8 w + d is
       // operand row d (D / 8) + w, so that a warp's chunks of one d lie in consecutive rows (different banks)
       if (!mbar_wait(&v_empty[vs], ((j / L::kV) & 1) ^ 1, p.err, abort_flag)) break;
-      uint8_t* vop = smem + L::offV + vs * L::kOp;
-#pragma unroll 1
-      for (int i = 0; i < 8 * kWords / 128; ++i) {
-        const int id = i * 128 + ut, w = id % kWords, kg = id / kWords;
+      {
+        static_assert(8 * kWords == kU, "a thread takes one word of 8 keys");
+        const int w = ut % kWords, kg = ut / kWords;
+        const uint8_t* src = raw + B::offV + 8 * kg * B::kRow + 4 * w;
+        uint8_t* dst = smem + L::offV + vs * L::kOp + (w >> 3) * 1024 + (w & 7) * 128 + ((kg ^ (w & 7)) << 4);
         uint32_t a[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          a[k] = ok ? *reinterpret_cast<const uint32_t*>(raw + B::offV + (8 * kg + k) * B::kRow + 4 * w) : 0x88888888u;
+        for (int k = 0; k < 8; ++k) a[k] = ok ? *reinterpret_cast<const uint32_t*>(src + k * B::kRow) : 0x88888888u;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint32_t sel = c | ((4 + c) << 8);
           uint32_t pr[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) pr[k] = prmt_b32(a[2 * k], a[2 * k + 1], sel);
-          const int n0 = 2 * c * kWords + w, n1 = n0 + kWords;
-          *reinterpret_cast<uint4*>(vop + (n0 >> 3) * 1024 + (n0 & 7) * 128 + ((kg ^ (n0 & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(dst + 2 * c * kWords * 128) =
               make_uint4(codes_lo(pr[0]), codes_lo(pr[1]), codes_lo(pr[2]), codes_lo(pr[3]));
-          *reinterpret_cast<uint4*>(vop + (n1 >> 3) * 1024 + (n1 & 7) * 128 + ((kg ^ (n1 & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(dst + (2 * c + 1) * kWords * 128) =
               make_uint4(codes_hi(pr[0]), codes_hi(pr[1]), codes_hi(pr[2]), codes_hi(pr[3]));
         }
       }
