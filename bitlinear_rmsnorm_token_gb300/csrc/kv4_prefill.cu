@@ -128,9 +128,10 @@ struct Layout {
   static constexpr int kUnpackWarps = D == 256 ? 8 : 4;
   static constexpr int kMeta = 4;
   static constexpr int kSoftWarps = 4 * kT;
-  static constexpr int kProducer = kSoftWarps + kUnpackWarps;
+  static constexpr int kProducer = kSoftWarps + kUnpackWarps;  // then an MMA warp per tile
   static constexpr int kMma0 = kProducer + 1;
-  static constexpr int kThreads = 32 * (kMma0 + kT);
+  static constexpr int kThreads = 512;
+  static_assert(kMma0 + kT <= kThreads / 32, "roles");
   static constexpr int kQPart = kRows * D * 2;               // bytes of one part of a tile's queries
   static constexpr int kOp = kKvPage * D * 2;                // bytes of a page's keys (values) as fp16
   static constexpr int offQ = 0;
@@ -138,7 +139,7 @@ struct Layout {
   static constexpr int offV = offK + kK * kOp;
   static constexpr int offRaw = offV + kV * kOp;
   static constexpr int offMeta = offRaw + kRaw * KvBlock<D>::kBytes;
-  static constexpr int kNumBars = 2 * kRaw + 2 * kK + 2 * kV + 2 * kMeta + 5 * kT;
+  static constexpr int kNumBars = 2 * kRaw + 2 * kK + 2 * kV + 2 * kMeta + 6 * kT;
   static constexpr int offBar = offMeta + kMeta * static_cast<int>(sizeof(PageMeta));
   static constexpr int offRow = offBar + kNumBars * 8;       // float2 per row: sum(q), its factor
   static constexpr int offMisc = offRow + kT * kRows * 8;    // 32 ints
@@ -182,10 +183,11 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
   uint64_t* p_full = s_full + 2 * kT;        // [tile]
   uint64_t* pv_done = p_full + kT;           // [tile]
   uint64_t* drained = pv_done + kT;          // [tile]: only on giving up
+  uint64_t* q_full = drained + kT;           // [tile]: the queries are in shared memory
   int* misc = reinterpret_cast<int*>(smem + L::offMisc);
   volatile int* abort_flag = misc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
-  // misc[2], misc[3]: sequence and pair of tiles; misc[8..]: running sums
+  // misc[2 .. 6]: sequence, pair of tiles, first row, rows and length; misc[8..]: running sums
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   pdl_launch_dependents();
@@ -193,64 +195,7 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
   const int head = blockIdx.x % p.c.heads;
   const int want = gridDim.x / p.c.heads - 1 - blockIdx.x / p.c.heads;
   if (threadIdx.x == 0) misc[2] = -1;
-  {
-    int base = 0;
-    for (int c0 = 0; c0 < p.c.num_seqs; c0 += L::kThreads) {
-      const int b = c0 + threadIdx.x;
-      int units = 0;
-      if (b < p.c.num_seqs) {
-        const int q0 = p.c.q_start[b];
-        const int64_t n = static_cast<int64_t>(p.c.q_start[b + 1]) - q0;
-        if (n < 0 || n > p.max_q || q0 < 0 || q0 + n > p.T) atomicOr(p.err, kErrBadIndex);
-        else units = static_cast<int>((n * p.G + kT * kRows - 1) / (kT * kRows));
-      }
-      int x = units;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) misc[8 + warp] = x;
-      __syncthreads();
-      int before = base;
-      for (int w = 0; w < L::kThreads / 32; ++w) {
-        if (w < warp) before += misc[8 + w];
-        base += misc[8 + w];
-      }
-      const int lo = before + x - units;
-      if (want >= lo && want < lo + units) {
-        misc[2] = b;
-        misc[3] = want - lo;
-      }
-    }
-  }
-  __syncthreads();
-  const int b = misc[2];
-  if (b < 0) return;  // the grid is sized for any division of the rows
-  bool bad = false;
-  const int len = kv_len_of(p.c, b, &bad);
-  if (bad && threadIdx.x == 0) atomicOr(p.err, kErrBadIndex);
-  const int q0 = p.c.q_start[b], n = p.c.q_start[b + 1] - q0;
-  const int row0 = misc[3] * kT * kRows;              // first row of the CTA
-  const int rows = n * p.G;
-  const int pos0 = len - n;                           // position of the sequence's first query token
-  // pages that any of the CTA's rows sees
-  int page0 = 0, pages = (len + kKvPage - 1) / kKvPage;
-  if (p.causal) {
-    const int last = pos0 + (min(row0 + kT * kRows, rows) - 1) / p.G;  // position of the last row
-    pages = last < 0 ? 0 : min(pages, last / kKvPage + 1);
-    if (p.window > 0) page0 = max(0, pos0 + row0 / p.G - p.window + 1) / kKvPage;
-  }
-  {
-    const int all = max(0, pages - page0);
-    const int z = blockIdx.z, Z = gridDim.z;
-    const int a = static_cast<int>(static_cast<int64_t>(all) * z / Z);
-    pages = static_cast<int>(static_cast<int64_t>(all) * (z + 1) / Z) - a;
-    page0 += a;
-  }
-
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32) {
     for (int i = 0; i < L::kRaw; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], L::kUnpackWarps);
@@ -273,65 +218,78 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&drained[i], 1);
+      mbar_init(&q_full[i], 4);
     }
     *abort_flag = 0;
     fence_barrier_init();
   }
+  {
+    int base = 0;
+    for (int c0 = 0; c0 < p.c.num_seqs; c0 += L::kThreads) {
+      const int i = c0 + threadIdx.x;
+      int units = 0, n_i = 0, q_i = 0, len_i = 0;
+      if (i < p.c.num_seqs) {
+        bool bad = false;
+        q_i = p.c.q_start[i];
+        const int64_t n64 = static_cast<int64_t>(p.c.q_start[i + 1]) - q_i;
+        len_i = kv_len_of(p.c, i, &bad);
+        if (n64 < 0 || n64 > p.max_q || q_i < 0 || q_i + n64 > p.T) bad = true;
+        else n_i = static_cast<int>(n64);
+        if (bad) atomicOr(p.err, kErrBadIndex);
+        units = (n_i * p.G + kT * kRows - 1) / (kT * kRows);
+      }
+      int x = units;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) misc[8 + warp] = x;
+      __syncthreads();
+      // running sums over the 16 warps, a lane each
+      int ws = lane < 16 ? misc[8 + lane] : 0;
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, ws, o);
+        if (lane >= o) ws += y;
+      }
+      const int total = __shfl_sync(0xffffffffu, ws, 15);
+      const int before = warp ? __shfl_sync(0xffffffffu, ws, warp - 1) : 0;
+      const int lo = base + before + x - units;
+      if (want >= lo && want < lo + units) {
+        misc[2] = i;
+        misc[3] = want - lo;
+        misc[4] = q_i;
+        misc[5] = n_i;
+        misc[6] = len_i;
+      }
+      base += total;
+    }
+  }
+  __syncthreads();
+  const int b = misc[2];
+  if (b < 0) return;  // the grid is sized for any division of the rows
   if (warp == L::kMma0) {
     tmem_alloc(tmem_slot, L::kCols);
     tmem_relinquish();
   }
-  // ---- queries, scaled by a power of two per row, as fp16 (one part or two): D / 8 lanes to a row, 8 dimensions each
-  float2* row_q = reinterpret_cast<float2*>(smem + L::offRow);
-  {
-    constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes of a row, rows of a warp at a time
-    constexpr int kStep = L::kThreads / 32 * kAt;
-    const int c = lane % kLanes;
-#pragma unroll 4
-    for (int rr = warp * kAt + lane / kLanes; rr < kT * kRows; rr += kStep) {
-      const int row = row0 + rr;
-      const bool on = row < rows;
-      const int i = on ? row / p.G : 0;
-      const QT* src = q + (static_cast<int64_t>(q0 + i) * p.Hq + head * p.G + (on ? row - i * p.G : 0)) * D + 8 * c;
-      float v[8];
-      const float4 a = on ? load4(src) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      const float4 b4 = on ? load4(src + 4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b4.x; v[5] = b4.y; v[6] = b4.z; v[7] = b4.w;
-      float top = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]));
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = pow2_exp(top);
-      const float f = p.sign * pow2(14 - e);
-      // chunk c of the row: dimensions 8c + 0, 4, 1, 5, 2, 6, 3, 7, the order in which a word of codes decodes
-      const int tl = rr / kRows, rt = rr % kRows;
-      uint8_t* dst = smem + L::offQ + tl * L::kParts * L::kQPart + (c >> 3) * (kRows * 128) + (rt >> 3) * 1024 +
-                     (rt & 7) * 128 + (((c & 7) ^ (rt & 7)) << 4);
-      float h[8], sum = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[k] *= f;
-        h[k] = __half2float(__float2half_rn(v[k]));
-        sum += h[k];
-      }
-      *reinterpret_cast<uint4*>(dst) =
-          make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
-      if constexpr (kSplit) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          h[k] = __half2float(__float2half_rn(v[k] - h[k]));
-          sum += h[k];
-        }
-        *reinterpret_cast<uint4*>(dst + L::kQPart) =
-            make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
-      }
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (c == 0) row_q[rr] = make_float2(sum, p.scale * pow2(e - 14));
-    }
-    fence_proxy_async_smem();
+  const int row0 = misc[3] * kT * kRows;              // first row of the CTA
+  const int q0 = misc[4], n = misc[5], len = misc[6];
+  const int rows = n * p.G;
+  const int pos0 = len - n;                           // position of the sequence's first query token
+  // pages that any of the CTA's rows sees
+  int page0 = 0, pages = (len + kKvPage - 1) / kKvPage;
+  if (p.causal) {
+    const int last = pos0 + (min(row0 + kT * kRows, rows) - 1) / p.G;  // position of the last row
+    pages = last < 0 ? 0 : min(pages, last / kKvPage + 1);
+    if (p.window > 0) page0 = max(0, pos0 + row0 / p.G - p.window + 1) / kKvPage;
+  }
+  pages = max(0, pages - page0);
+  if (gridDim.z > 1) {  // this part's pages (at most 2^25 pages and 64 parts: 32 bits)
+    const unsigned all = pages, a = all * blockIdx.z / gridDim.z;
+    pages = static_cast<int>(all * (blockIdx.z + 1) / gridDim.z - a);
+    page0 += static_cast<int>(a);
   }
   tc_fence_before();
   __syncthreads();
@@ -342,6 +300,71 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
     // ------------------------------------------------------------ softmax
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;  // this warp's quarter of the TMEM lanes
     const int tile = warp >> 2;
+    // ---- queries, scaled by a power of two per row, as fp16 (one part or two): D / 8 lanes to a row, 8 dimensions
+    // each, the loads of 8 rows in flight
+    float2* row_q = reinterpret_cast<float2*>(smem + L::offRow);
+    {
+      constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes of a row, rows of a warp at a time
+      constexpr int kStep = 4 * kAt, kBatch = 8;
+      constexpr int kVecs = sizeof(QT) / 2;             // 16-byte loads of 8 dimensions
+      const int c = lane % kLanes;
+#pragma unroll 1
+      for (int t0 = (warp & 3) * kAt + lane / kLanes; t0 < kRows; t0 += kBatch * kStep) {
+        uint4 raw[kBatch][kVecs];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int row = row0 + tile * kRows + t0 + k * kStep;
+          const int i = row / p.G;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              q + (static_cast<int64_t>(q0 + i) * p.Hq + head * p.G + (row - i * p.G)) * D + 8 * c);
+#pragma unroll
+          for (int u = 0; u < kVecs; ++u) raw[k][u] = row < rows ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int rt = t0 + k * kStep;
+          const QT* x = reinterpret_cast<const QT*>(raw[k]);
+          float v[8], top = 0.0f;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            v[d] = static_cast<float>(x[d]);
+            top = fmaxf(top, fabsf(v[d]));
+          }
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int e = pow2_exp(top);
+          const float f = p.sign * pow2(14 - e);
+          // chunk c of the row: dimensions 8c + 0, 4, 1, 5, 2, 6, 3, 7, the order in which a word of codes decodes
+          uint8_t* dst = smem + L::offQ + tile * L::kParts * L::kQPart + (c >> 3) * (kRows * 128) + (rt >> 3) * 1024 +
+                         (rt & 7) * 128 + (((c & 7) ^ (rt & 7)) << 4);
+          float h[8], sum = 0.0f;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            v[d] *= f;
+            h[d] = __half2float(__float2half_rn(v[d]));
+            sum += h[d];
+          }
+          *reinterpret_cast<uint4*>(dst) =
+              make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
+          if constexpr (kSplit) {
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              h[d] = __half2float(__float2half_rn(v[d] - h[d]));
+              sum += h[d];
+            }
+            *reinterpret_cast<uint4*>(dst + L::kQPart) =
+                make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
+          }
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (c == 0) row_q[tile * kRows + rt] = make_float2(sum, p.scale * pow2(e - 14));
+        }
+      }
+      fence_proxy_async_smem();
+    }
+    // the tile's four warps meet: a thread reads its row's factors, which another warp may have written
+    asm volatile("bar.sync %0, 128;" ::"r"(tile + 1) : "memory");
+    if (lane == 0) mbar_arrive(&q_full[tile]);
     const int tile_r0 = row0 + tile * kRows;
     const int r = tile_r0 + (threadIdx.x & 127);  // row of the item
     const bool row_on = r < rows;
@@ -670,7 +693,7 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ MMA issue, a warp per tile
-    if (lane == 0) {
+    if (warp < L::kMma0 + kT && lane == 0) {
       const int t = warp - L::kMma0;
       constexpr uint32_t id_s = idesc_f16_f32(kRows, kKvPage), id_o = idesc_f16_f32(kRows, D);
       const uint32_t q_addr = smem_u32(smem + L::offQ + t * L::kParts * L::kQPart);
@@ -692,7 +715,7 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
         tc_commit(&k_empty[ks]);
         return true;
       };
-      bool ok = pages == 0 || scores(0);
+      bool ok = pages == 0 || (mbar_wait(&q_full[t], 0, p.err, abort_flag) && scores(0));
       for (int j = 0; ok && j < pages; ++j) {
         if (j + 1 < pages) {
           // the other score buffer holds W of the page before: its product must be done with it
