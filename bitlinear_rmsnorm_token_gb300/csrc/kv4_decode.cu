@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(L::kThreads, 1)
         }
       }
       if (!mbar_wait(&full[slot], phase, p.err, abort_flag)) break;
+      __syncwarp();
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1;
@@ -536,31 +537,33 @@ __global__ void __launch_bounds__(L::kThreads, 1)
               z += __shfl_xor_sync(0xffffffffu, z, o);
             }
             const int r = nb * kRowsNb + (kSplit ? t : 2 * t + j);
-            if (r >= rows) continue;
-            float o[2 * kTiles];
+            if (r < rows) {
+              float o[2 * kTiles];
 #pragma unroll
-            for (int i = 0; i < 2 * kTiles; ++i) o[i] = acc[nb][i][j] + z;
-            if (un.flags & kWhole) {
-              const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // no key seen: zeros; NaN stays
-              const int i_tok = r / p.G;
-              OT* dst = out + (static_cast<int64_t>(un.q0 + i_tok) * p.Hq + un.head * p.G + (r - i_tok * p.G)) * D +
-                        2 * kTiles * g;
-              constexpr int kPer = 16 / static_cast<int>(sizeof(OT));
+              for (int i = 0; i < 2 * kTiles; ++i) o[i] = acc[nb][i][j] + z;
+              if (un.flags & kWhole) {
+                const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // no key seen: zeros; NaN stays
+                const int i_tok = r / p.G;
+                OT* dst = out + (static_cast<int64_t>(un.q0 + i_tok) * p.Hq + un.head * p.G + (r - i_tok * p.G)) * D +
+                          2 * kTiles * g;
+                constexpr int kPer = 16 / static_cast<int>(sizeof(OT));
 #pragma unroll
-              for (int i = 0; i < 2 * kTiles / kPer; ++i) {
-                union { OT v[kPer]; uint4 u; } pk;
+                for (int i = 0; i < 2 * kTiles / kPer; ++i) {
+                  union { OT v[kPer]; uint4 u; } pk;
 #pragma unroll
-                for (int c = 0; c < kPer; ++c) pk.v[c] = round_out<OT>(o[i * kPer + c] * inv);
-                reinterpret_cast<uint4*>(dst)[i] = pk.u;
+                  for (int c = 0; c < kPer; ++c) pk.v[c] = round_out<OT>(o[i * kPer + c] * inv);
+                  reinterpret_cast<uint4*>(dst)[i] = pk.u;
+                }
+              } else {
+                float* dst = p.part + ((static_cast<int64_t>(un.item) + w_me) * p.rows + r) * (D + 4);
+#pragma unroll
+                for (int i = 0; i < kTiles / 2; ++i)
+                  reinterpret_cast<float4*>(dst + 2 * kTiles * g)[i] =
+                      make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                if (g == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(m_run[nb][j], l);
               }
-            } else {
-              float* dst = p.part + ((static_cast<int64_t>(un.item) + w_me) * p.rows + r) * (D + 4);
-#pragma unroll
-              for (int i = 0; i < kTiles / 2; ++i)
-                reinterpret_cast<float4*>(dst + 2 * kTiles * g)[i] =
-                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-              if (g == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(m_run[nb][j], l);
             }
+            __syncwarp();
           }
       }
     }

@@ -12,7 +12,7 @@
 // with C the cache's codes as c - 8 in fp16, exact; the scales stay out of the
 // products (kv4.cuh).  O, S and W live in tensor memory; W takes S's place.
 // A row's reference only moves when its maximum has grown by 2^8 (O is then
-// rescaled); W is kept in fp16's range by a power of two of the largest value
+// rescaled), so most pages are taken without a maximum, scores to W in one pass; W is kept in fp16's range by a power of two of the largest value
 // scale met, which moves in the same way.  fp32 queries and their W are two fp16
 // parts each (22 bits), two products where 16-bit ones take one.
 //
@@ -101,12 +101,6 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, 
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld_32x32b_x4(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(taddr)
-               : "memory");
-}
 
 // A page's per-key factors, and what the softmax has to know of the page.
 struct __align__(16) PageMeta {
@@ -139,7 +133,7 @@ struct Layout {
   static constexpr int offV = offK + kK * kOp;
   static constexpr int offRaw = offV + kV * kOp;
   static constexpr int offMeta = offRaw + kRaw * KvBlock<D>::kBytes;
-  static constexpr int kNumBars = 2 * kRaw + 2 * kK + 2 * kV + 2 * kMeta + 6 * kT;
+  static constexpr int kNumBars = 2 * kRaw + 2 * kK + 2 * kV + 2 * kMeta + 8 * kT;
   static constexpr int offBar = offMeta + kMeta * static_cast<int>(sizeof(PageMeta));
   static constexpr int offRow = offBar + kNumBars * 8;       // float2 per row: sum(q), its factor
   static constexpr int offMisc = offRow + kT * kRows * 8;    // 32 ints
@@ -180,10 +174,12 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
   uint64_t* meta_full = v_empty + L::kV;
   uint64_t* meta_empty = meta_full + L::kMeta;
   uint64_t* s_full = meta_empty + L::kMeta;  // [tile][buffer]
-  uint64_t* p_full = s_full + 2 * kT;        // [tile]
-  uint64_t* pv_done = p_full + kT;           // [tile]
+  // [tile][buffer]: a warp may be done with page j + 1 before another is with page j, but not with page j + 2
+  uint64_t* p_full = s_full + 2 * kT;
+  uint64_t* pv_done = p_full + 2 * kT;       // [tile]
   uint64_t* drained = pv_done + kT;          // [tile]: only on giving up
   uint64_t* q_full = drained + kT;           // [tile]: the queries are in shared memory
+  uint64_t* o_done = q_full + kT;            // [tile]: the last product is done
   int* misc = reinterpret_cast<int*>(smem + L::offMisc);
   volatile int* abort_flag = misc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
@@ -215,10 +211,12 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
     for (int i = 0; i < kT; ++i) {
       mbar_init(&s_full[2 * i], 1);
       mbar_init(&s_full[2 * i + 1], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&drained[i], 1);
       mbar_init(&q_full[i], 4);
+      mbar_init(&o_done[i], 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -383,18 +381,79 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
     f2 l2 = 0, z2 = 0;  // sums of the even and of the odd keys
     int e_run = 0;
     bool ok = true;
-    // A page's share of the softmax; kMasked: some key of it is hidden from some row of the tile.
+    // O by f, once the product before page j is done with it.
+    auto rescale = [&](int j, float f) -> bool {
+      if (!mbar_wait(&pv_done[tile], (j - 1) & 1, p.err, abort_flag)) return false;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        uint32_t o[16];
+        tmem_read_x16(tmem + lanes + static_cast<uint32_t>(L::o_col(tile) + c), o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tmem_st_32x32b_x16(tmem + lanes + static_cast<uint32_t>(L::o_col(tile) + c), o);
+      }
+      tmem_st_wait();
+      return true;
+    };
+    // A page that every row of the warp sees whole, against the references as they are: no maximum is taken. A row's
+    // sum above 2^kLazy (as every probability above it makes) gives the page back to the other path, which moves the
+    // reference; otherwise each probability is within what W holds.  1: done, 0: not taken, -1: gave up.
+    auto page_fast = [&](int j, uint32_t s_addr, const PageMeta& meta) -> int {
+      const f2 ref2 = f2_pack(-m_ref, -m_ref);
+      f2 lp = 0, zp = 0;
+      uint32_t w0[32];
+      [[maybe_unused]] uint32_t w1[32];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t sv[32];
+        tmem_read_x32(s_addr + 32 * hf, sv);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(&meta.ks[32 * hf + 2 * i]);
+          const ulonglong2 km = *reinterpret_cast<const ulonglong2*>(&meta.kmid[32 * hf + 2 * i]);
+          const ulonglong2 vs = *reinterpret_cast<const ulonglong2*>(&meta.vs[32 * hf + 2 * i]);
+          const ulonglong2 vm = *reinterpret_cast<const ulonglong2*>(&meta.vmid[32 * hf + 2 * i]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const f2 sp = f2_pack(__uint_as_float(sv[2 * (i + k)]), __uint_as_float(sv[2 * (i + k) + 1]));
+            const f2 x = f2_fma(sp, k ? ks.y : ks.x, f2_mul(k ? km.y : km.x, qsum2));
+            float a, b;
+            f2_unpack(f2_fma(x, qc2, ref2), a, b);
+            const f2 pr = f2_pack(ex2(a), ex2(b));
+            lp = f2_add(lp, pr);
+            zp = f2_fma(pr, k ? vm.y : vm.x, zp);
+            float wa, wb;
+            f2_unpack(f2_mul(pr, k ? vs.y : vs.x), wa, wb);
+            const int at = 16 * hf + i + k;
+            w0[at] = pack_h2(wa, wb);
+            if constexpr (kSplit) {
+              const __half2 h = *reinterpret_cast<const __half2*>(&w0[at]);
+              w1[at] = pack_h2(wa - __low2float(h), wb - __high2float(h));
+            }
+          }
+        }
+      }
+      float a, b;
+      f2_unpack(lp, a, b);
+      if (__any_sync(0xffffffffu, a + b > 256.0f)) return 0;  // 2^kLazy
+      l2 = f2_add(l2, lp);
+      z2 = f2_add(z2, zp);
+      if (meta.grow && !rescale(j, pow2(-meta.grow))) return -1;
+      tmem_st_32x32b_x32(s_addr, w0);
+      if constexpr (kSplit) tmem_st_32x32b_x32(s_addr + 32, w1);
+      tmem_st_wait();
+      return 1;
+    };
+    // Any page; kMasked: some key of it is hidden from some row of the tile.
     auto page = [&](int j, uint32_t s_addr, const PageMeta& meta, auto masked_tag) -> bool {
       constexpr bool kMasked = decltype(masked_tag)::value;
       f2 x[32];
       float top = -INFINITY;
       {
         uint32_t s0[32], s1[32];
-        tmem_ld_32x32b_x32(s_addr, s0);
-        tmem_ld_32x32b_x32(s_addr + 32, s1);
-        tmem_ld_wait();
-        tmem_reg_fence(s0);
-        tmem_reg_fence(s1);
+        tmem_read_x32(s_addr, s0);
+        tmem_read_x32(s_addr + 32, s1);
         [[maybe_unused]] const int hi = meta.ok ? key_hi - meta.key0 : -1, lo = key_lo - meta.key0;
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
@@ -432,24 +491,12 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
         }
       }
       if (meta.grow) f *= pow2(-meta.grow);
-      if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-        if (!mbar_wait(&pv_done[tile], (j - 1) & 1, p.err, abort_flag)) return false;
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16];
-          tmem_ld_32x32b_x16(tmem + lanes + static_cast<uint32_t>(L::o_col(tile) + c), o);
-          tmem_ld_wait();
-          tmem_reg_fence16(o);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st_32x32b_x16(tmem + lanes + static_cast<uint32_t>(L::o_col(tile) + c), o);
-        }
-        tmem_st_wait();
-      }
+      if (j > 0 && __any_sync(0xffffffffu, f != 1.0f) && !rescale(j, f)) return false;
       // ---- probabilities, sums, and W over the scores, 32 keys at a time
+      // (the sums in the order of the other path: a row's bits do not depend on the rows beside it)
       const float ref = m_ref == -INFINITY ? 0.0f : -m_ref;
       const f2 ref2 = f2_pack(ref, ref);
+      f2 lp = 0, zp = 0;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         uint32_t w0[16];
@@ -465,20 +512,21 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
             f2_unpack(f2_fma(xi, qc2, ref2), a, b);
             a = ex2(a);
             b = ex2(b);
-            f2 pr = f2_pack(a, b), w = f2_mul(pr, k ? vs.y : vs.x), zi = f2_mul(pr, k ? vm.y : vm.x);
+            f2 vmk = k ? vm.y : vm.x;
+            f2 pr = f2_pack(a, b), w = f2_mul(pr, k ? vs.y : vs.x);
             if constexpr (kMasked) {  // whatever the value row of a masked key holds
-              float xa, xb, za, zb;
+              float xa, xb, ma, mb;
               f2_unpack(xi, xa, xb);
               f2_unpack(w, wa, wb);
-              f2_unpack(zi, za, zb);
-              if (xa == -INFINITY) a = wa = za = 0.0f;
-              if (xb == -INFINITY) b = wb = zb = 0.0f;
+              f2_unpack(vmk, ma, mb);
+              if (xa == -INFINITY) a = wa = ma = 0.0f;
+              if (xb == -INFINITY) b = wb = mb = 0.0f;
               pr = f2_pack(a, b);
               w = f2_pack(wa, wb);
-              zi = f2_pack(za, zb);
+              vmk = f2_pack(ma, mb);
             }
-            l2 = f2_add(l2, pr);
-            z2 = f2_add(z2, zi);
+            lp = f2_add(lp, pr);
+            zp = f2_fma(pr, vmk, zp);
             f2_unpack(w, wa, wb);
             w0[i + k] = pack_h2(wa, wb);
             if constexpr (kSplit) {
@@ -490,6 +538,8 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
         tmem_st_32x32b_x16(s_addr + 16 * hf, w0);
         if constexpr (kSplit) tmem_st_32x32b_x16(s_addr + 32 + 16 * hf, w1);
       }
+      l2 = f2_add(l2, lp);
+      z2 = f2_add(z2, zp);
       tmem_st_wait();
       return true;
     };
@@ -502,15 +552,19 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
         break;
       }
       tc_fence_after();
+      __syncwarp();
       const PageMeta& meta = metas[ms];
       e_run = meta.e;
       const bool masked = !meta.ok || meta.key0 < free_lo || meta.key0 + kKvPage - 1 > free_hi;
-      ok = masked ? page(j, s_addr, meta, std::true_type{}) : page(j, s_addr, meta, std::false_type{});
+      int done = 0;
+      if (!masked && __all_sync(0xffffffffu, m_ref != -INFINITY)) done = page_fast(j, s_addr, meta);
+      ok = done > 0 || (done == 0 && (masked ? page(j, s_addr, meta, std::true_type{})
+                                             : page(j, s_addr, meta, std::false_type{})));
       if (!ok) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&p_full[tile]);
+        mbar_arrive(&p_full[2 * tile + buf]);
         mbar_arrive(&meta_empty[ms]);
       }
     }
@@ -523,8 +577,10 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
       z = a + b;
     }
     // ---- the row's result
-    if (ok && (pages == 0 || mbar_wait(&pv_done[tile], (pages - 1) & 1, p.err, abort_flag))) {
+    // (a barrier of its own: this warp may be up to two products ahead of pv_done, whose parity says nothing then)
+    if (ok && (pages == 0 || mbar_wait(&o_done[tile], 0, p.err, abort_flag))) {
       tc_fence_after();
+      __syncwarp();
       const float un_w = pow2(e_run - kWExp);
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // no key seen: zeros; NaN stays
       const bool any_on = tile_r0 + 32 * (warp & 3) < rows;
@@ -533,35 +589,31 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
         for (int a = 0; a < D / 32; ++a) {
           // dimensions 32 a ..: columns d (D / 8) + 4 a .. + 3 hold dimension d of the groups of 8
           uint32_t o[32];
-          if (pages > 0) {
+          if (pages > 0) tmem_read_8x4(tmem + lanes + static_cast<uint32_t>(L::o_col(tile) + 4 * a), D / 8, o);
+          if (row_on) {
+            float v[32];
 #pragma unroll
-            for (int d = 0; d < 8; ++d)
-              tmem_ld_32x32b_x4(tmem + lanes + static_cast<uint32_t>(L::o_col(tile) + d * (D / 8) + 4 * a), o + 4 * d);
-            tmem_ld_wait();
-            tmem_reg_fence(o);
-          }
-          if (!row_on) continue;
-          float v[32];
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+              for (int d = 0; d < 8; ++d) v[8 * k + d] = pages > 0 ? fmaf(__uint_as_float(o[4 * d + k]), un_w, z) : 0.0f;
+            if (p.part) {
+              float* dst = p.part + (static_cast<int64_t>(blockIdx.z) * p.T * p.Hq + q_at) * (D + 4) + 32 * a;
 #pragma unroll
-            for (int d = 0; d < 8; ++d) v[8 * k + d] = pages > 0 ? fmaf(__uint_as_float(o[4 * d + k]), un_w, z) : 0.0f;
-          if (p.part) {
-            float* dst = p.part + (static_cast<int64_t>(blockIdx.z) * p.T * p.Hq + q_at) * (D + 4) + 32 * a;
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<float4*>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            } else {
+              OT* dst = out + q_at * D + 32 * a;
+              constexpr int kPer = 16 / static_cast<int>(sizeof(OT));
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<float4*>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          } else {
-            OT* dst = out + q_at * D + 32 * a;
-            constexpr int kPer = 16 / static_cast<int>(sizeof(OT));
+              for (int i = 0; i < 32 / kPer; ++i) {
+                union { OT v[kPer]; uint4 u; } pk;
 #pragma unroll
-            for (int i = 0; i < 32 / kPer; ++i) {
-              union { OT v[kPer]; uint4 u; } pk;
-#pragma unroll
-              for (int k = 0; k < kPer; ++k) pk.v[k] = round_out<OT>(v[i * kPer + k] * inv);
-              reinterpret_cast<uint4*>(dst)[i] = pk.u;
+                for (int k = 0; k < kPer; ++k) pk.v[k] = round_out<OT>(v[i * kPer + k] * inv);
+                reinterpret_cast<uint4*>(dst)[i] = pk.u;
+              }
             }
           }
+          __syncwarp();  // the next load is the whole warp's
         }
         if (p.part && row_on)
           *reinterpret_cast<float2*>(p.part + (static_cast<int64_t>(blockIdx.z) * p.T * p.Hq + q_at) * (D + 4) + D) =
@@ -724,7 +776,7 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
         }
         const int vs = j % L::kV;
         if (!mbar_wait(&v_full[vs], (j / L::kV) & 1, p.err, abort_flag)) break;
-        if (!mbar_wait(&p_full[t], j & 1, p.err, abort_flag)) break;
+        if (!mbar_wait(&p_full[2 * t + (j & 1)], (j >> 1) & 1, p.err, abort_flag)) break;
         tc_fence_after();
         const uint32_t v_addr = smem_u32(smem + L::offV + vs * L::kOp);
 #pragma unroll
@@ -734,7 +786,7 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
             tc_mma_f16_ta(tmem + static_cast<uint32_t>(L::o_col(t)),
                           tmem + static_cast<uint32_t>(L::s_col(t, j & 1) + 32 * part + 8 * k),
                           sw128_kmajor_desc(v_addr) + 2 * k, id_o, (j | part | k) != 0 ? 1u : 0u);
-        tc_commit(&pv_done[t]);
+        tc_commit(j + 1 < pages ? &pv_done[t] : &o_done[t]);
         tc_commit(&v_empty[vs]);
       }
       if (*abort_flag) {  // given up: the products in flight must end before shared and tensor memory go

@@ -310,12 +310,11 @@ __global__ void __launch_bounds__(Layout<BN>::kThreads, 1)
               break;
             }
             tc_fence_after();
+            __syncwarp();
 #pragma unroll
             for (int k0 = 0; k0 < L::kEpiCols; k0 += 16) {
               uint32_t v[16];
-              tmem_ld_32x32b_x16(tq + static_cast<uint32_t>(buf * BN + k0), v);
-              tmem_ld_wait();
-              tmem_reg_fence16(v);
+              tmem_read_x16(tq + static_cast<uint32_t>(buf * BN + k0), v);
 #pragma unroll
               for (int k = 0; k < 16; ++k) acc[k0 + k] += __float2int_rn(__uint_as_float(v[k]));
             }

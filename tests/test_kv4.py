@@ -290,6 +290,20 @@ def test_many_tokens(device, D, Hkv, G, dtype, causal):
 
 
 @gpu
+def test_many_tokens_again_and_again(device):
+    """The same bits from run to run with many pages and tiles in flight: no warp may pass another's page."""
+    for D, Hkv, G in ((128, 4, 4), (256, 2, 4)):
+        c = ref.Case(26, [200, 90, 300], [1500, 2000, 300], Hkv, D)
+        d = c.dev()
+        for dtype in (F32, BF16):
+            q = queries(27, c.T, Hkv * G, D, dtype).cuda()
+            want = run_attention(c, d, q, G)
+            assert torch.isfinite(want).all()
+            for _ in range(40):
+                assert torch.equal(run_attention(c, d, q, G), want)
+
+
+@gpu
 @pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 100, 100000])
 @pytest.mark.parametrize("counts,lens", [([1, 1, 1, 1], [1, 64, 100, 1000]), ([5, 5, 5], [5, 70, 500]),
                                          ([150, 40], [150, 400])])
