@@ -6,28 +6,20 @@
 // h G + r % G of token r / G, so the heads that share keys share the tile.  A CTA
 // takes two tiles (head_dim 128) or one (256) and walks the pages that their rows
 // see, 64 keys at a time, with the running maximum and sum of a one-pass softmax:
-//   S[128, 64]  = Q K^T   (tcgen05, fp16 operands, both in shared memory)
-//   p = 2^(c S - ref)
-//   O[128, D] += W V      (W from tensor memory)
-// O, S and W live in tensor memory; W takes S's place.  A row's reference only
-// moves when its maximum has grown by 2^8 (O is then rescaled), so most pages are
-// taken without a maximum, scores to W in one pass.
+//   S[128, 64]  = Q C_k^T   (tcgen05, fp16 operands, both in shared memory)
+//   x = s_j S + (m_j + 8 s_j) sum(q), p = 2^(c x - ref)
+//   O[128, D] += W C_v      (W = p s_j as fp16 from tensor memory)
+// with C the cache's codes as c - 8 in fp16, exact; the scales stay out of the
+// products (kv4.cuh).  O, S and W live in tensor memory; W takes S's place.
+// A row's reference only moves when its maximum has grown by 2^8 (O is then
+// rescaled), so most pages are taken without a maximum, scores to W in one pass; W is kept in fp16's range by a power of two of the largest value
+// scale met, which moves in the same way.  fp32 queries and their W are two fp16
+// parts each (22 bits), two products where 16-bit ones take one.
 //
-// What stands for K and V depends on the query type:
-//   bf16: the stored values rounded to fp16 (11 bits: 1/8 of the rounding that the
-//     queries and the output have), times a power of two of the page's largest
-//     key and of the largest value met; W = p as fp16.  c S is one fma, and the
-//     softmax, which sets the pace, has 5 instructions a pair of scores instead of
-//     11 (chunk of 4096 over 12288 tokens: see the last line).
-//   fp16, fp32: the codes as c - 8, exact, with the scales outside the products
-//     (kv4.cuh): x = s_j S + (m_j + 8 s_j) sum(q), W = p s_j times a power of two,
-//     and sum p_j (m_j + 8 s_j) beside O.  fp32 queries and their W are two fp16
-//     parts each (22 bits), two products where 16-bit ones take one.
-//
-// Warps: 4 per tile for the softmax (a thread a row), 8 or 12 that decode pages
-// into the operands' swizzled layout (values transposed: rows are dimensions, in
-// the order that keeps the stores of a warp on different banks), a producer of
-// raw pages, and an MMA issuer per tile.  S is double buffered, so that the next
+// Warps: 4 per tile for the softmax (a thread a row), 4 that decode pages into
+// the operands' swizzled layout (values transposed: rows are dimensions, in the
+// order that keeps the stores of a warp on different banks), a producer of raw
+// pages, and an MMA issuer per tile.  S is double buffered, so that the next
 // page's scores are computed while a page's softmax runs.
 // Few tiles on a long cache: the pages are split over gridDim.z and the parts
 // joined by a second launch, in order.
@@ -110,52 +102,30 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, 
       : "memory");
 }
 
-// c s + mid of two codes, s in two parts: one rounding of the sum (and of mid).
-__device__ __forceinline__ uint32_t decode_h2(uint32_t c, uint32_t hi, uint32_t lo, uint32_t mid) {
-  const __half2 x = *reinterpret_cast<const __half2*>(&c);
-  const __half2 t = __hfma2(x, *reinterpret_cast<const __half2*>(&lo), *reinterpret_cast<const __half2*>(&mid));
-  const __half2 r = __hfma2(x, *reinterpret_cast<const __half2*>(&hi), t);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // A page's per-key factors, and what the softmax has to know of the page.
 struct __align__(16) PageMeta {
   float ks[kKvPage], kmid[kKvPage];  // s, m + 8 s of the keys
   float vs[kKvPage], vmid[kKvPage];  // s 2^(kWExp - e), m + 8 s of the values
   int key0;           // position of the page's first token
   int ok;             // 0: no such page, its keys are masked
-  int e;              // the power of two that the value scales (bf16: values) lie below
-  float gk;           // bf16: what a unit of S counts (the keys' power of two)
+  int grow;           // e has grown by this much since the page before
+  int e;
 };
 
-// bf16: s (two parts) and m + 8 s of a page's rows as fp16, times the operands' powers of two; zeros for tokens that do
-// not exist and for rows that are not finite (they stand for unspecified values, and must not reach other queries).
-struct __align__(16) PageTab {
-  uint4 k[kKvPage];  // each twice, for both halves of a word: s high, s low, m + 8 s
-  __half v_hi[kKvPage], v_lo[kKvPage], v_mid[kKvPage];
-};
-
-template <int D, bool kSplit, bool kDeq>
+template <int D, bool kSplit>
 struct Layout {
   static constexpr int kT = D == 128 ? 2 : 1;                // tiles per CTA
   static constexpr int kParts = kSplit ? 2 : 1;
-  // Decode warps: heads of 128, groups of 4 that take every kGroups-th page each; heads of 256, 8 that decode the keys
-  // of every page and 4 the values.  Raw page slots (whole turns of the groups) and operand stages (at least a turn):
-  // no group can then be a phase ahead of what a barrier's parity tells.
-  static constexpr bool kByRole = D == 256;
-  static constexpr int kGroups = D == 128 && !kSplit ? 2 : 1;
-  static constexpr int kKeyWarps = kByRole ? 8 : 4, kValWarps = 4;
-  static constexpr int kDecodeWarps = kByRole ? kKeyWarps + kValWarps : 4 * kGroups;
-  static constexpr int kPageWarps = kByRole ? kDecodeWarps : 4;  // warps that take part in a page
-  static constexpr int kRaw = D == 128 ? (kSplit ? 2 : 4) : (kSplit ? 1 : 2);
-  static constexpr int kK = D == 128 ? (kSplit ? 2 : 3) : 1;
-  static constexpr int kV = D == 128 ? (kSplit ? 2 : 3) : (kSplit ? 1 : 2);
-  static_assert(kRaw % kGroups == 0 && kK >= kGroups && kV >= kGroups, "see above");
+  static constexpr int kRaw = D == 256 && kSplit ? 1 : 2;    // raw page slots
+  static constexpr int kK = D == 256 ? 1 : 2;                // key operand stages
+  static constexpr int kV = D == 256 && kSplit ? 1 : 2;      // value operand stages
+  static constexpr int kUnpackWarps = D == 256 ? 8 : 4;
   static constexpr int kMeta = 4;
   static constexpr int kSoftWarps = 4 * kT;
-  static constexpr int kProducer = kSoftWarps + kDecodeWarps;  // then an MMA warp per tile
+  static constexpr int kProducer = kSoftWarps + kUnpackWarps;  // then an MMA warp per tile
   static constexpr int kMma0 = kProducer + 1;
-  static constexpr int kThreads = 32 * (kMma0 + kT);
+  static constexpr int kThreads = 512;
+  static_assert(kMma0 + kT <= kThreads / 32, "roles");
   static constexpr int kQPart = kRows * D * 2;               // bytes of one part of a tile's queries
   static constexpr int kOp = kKvPage * D * 2;                // bytes of a page's keys (values) as fp16
   static constexpr int offQ = 0;
@@ -163,12 +133,11 @@ struct Layout {
   static constexpr int offV = offK + kK * kOp;
   static constexpr int offRaw = offV + kV * kOp;
   static constexpr int offMeta = offRaw + kRaw * KvBlock<D>::kBytes;
-  static constexpr int kNumBars = 2 * kRaw + 2 * kK + 2 * kV + 2 * kMeta + 7 * kT + 4;
+  static constexpr int kNumBars = 2 * kRaw + 2 * kK + 2 * kV + 2 * kMeta + 8 * kT;
   static constexpr int offBar = offMeta + kMeta * static_cast<int>(sizeof(PageMeta));
   static constexpr int offRow = offBar + kNumBars * 8;       // float2 per row: sum(q), its factor
-  static constexpr int offTab = (offRow + kT * kRows * 8 + 15) / 16 * 16;  // two pages' factors of each group
-  static constexpr int offMisc = offTab + (kDeq ? 2 * kGroups * static_cast<int>(sizeof(PageTab)) : 0);  // 48 ints
-  static constexpr int kBytes = offMisc + 192;
+  static constexpr int offMisc = offRow + kT * kRows * 8;    // 32 ints
+  static constexpr int kBytes = offMisc + 128;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 232448, "over the 227 KB of shared memory a CTA may use");
   // tensor memory: scores (two buffers) and output of each tile
@@ -187,12 +156,10 @@ struct Problem {
   float* part;  // [splits][T * Hq][D + 4], or null
 };
 
-template <int D, typename QT, typename OT>
-__global__ void __launch_bounds__(
-    Layout<D, std::is_same<QT, float>::value, std::is_same<QT, __nv_bfloat16>::value>::kThreads, 1)
+template <int D, bool kSplit, typename QT, typename OT>
+__global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
     k_kv4_prefill(const Problem p, const QT* __restrict__ q, OT* __restrict__ out) {
-  constexpr bool kSplit = std::is_same<QT, float>::value, kDeq = std::is_same<QT, __nv_bfloat16>::value;
-  using L = Layout<D, kSplit, kDeq>;
+  using L = Layout<D, kSplit>;
   using B = KvBlock<D>;
   constexpr int kT = L::kT;
   extern __shared__ uint8_t smem_raw[];
@@ -211,8 +178,8 @@ __global__ void __launch_bounds__(
   uint64_t* p_full = s_full + 2 * kT;
   uint64_t* pv_done = p_full + 2 * kT;       // [tile]
   uint64_t* drained = pv_done + kT;          // [tile]: only on giving up
-  uint64_t* tab_full = drained + kT;         // [group or role][2]: the table of factors is written (bf16)
-  uint64_t* o_done = tab_full + 4;            // [tile]: the last product is done
+  uint64_t* q_full = drained + kT;           // [tile]: the queries are in shared memory
+  uint64_t* o_done = q_full + kT;            // [tile]: the last product is done
   int* misc = reinterpret_cast<int*>(smem + L::offMisc);
   volatile int* abort_flag = misc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
@@ -227,19 +194,18 @@ __global__ void __launch_bounds__(
   if (threadIdx.x == 32) {
     for (int i = 0; i < L::kRaw; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], L::kPageWarps);
+      mbar_init(&raw_empty[i], L::kUnpackWarps);
     }
     for (int i = 0; i < L::kK; ++i) {
-      mbar_init(&k_full[i], L::kKeyWarps);
+      mbar_init(&k_full[i], L::kUnpackWarps);
       mbar_init(&k_empty[i], kT);
     }
     for (int i = 0; i < L::kV; ++i) {
-      mbar_init(&v_full[i], L::kValWarps);
+      mbar_init(&v_full[i], L::kUnpackWarps);
       mbar_init(&v_empty[i], kT);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&tab_full[i], i < 2 ? L::kKeyWarps : L::kValWarps);
     for (int i = 0; i < L::kMeta; ++i) {
-      mbar_init(&meta_full[i], L::kPageWarps);
+      mbar_init(&meta_full[i], L::kUnpackWarps);
       mbar_init(&meta_empty[i], L::kSoftWarps);
     }
     for (int i = 0; i < kT; ++i) {
@@ -249,6 +215,7 @@ __global__ void __launch_bounds__(
       mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&drained[i], 1);
+      mbar_init(&q_full[i], 4);
       mbar_init(&o_done[i], 1);
     }
     *abort_flag = 0;
@@ -278,14 +245,14 @@ __global__ void __launch_bounds__(
       __syncthreads();
       if (lane == 31) misc[8 + warp] = x;
       __syncthreads();
-      // running sums over the warps, a lane each
-      int ws = lane < L::kThreads / 32 ? misc[8 + lane] : 0;
+      // running sums over the 16 warps, a lane each
+      int ws = lane < 16 ? misc[8 + lane] : 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
+      for (int o = 1; o < 16; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, ws, o);
         if (lane >= o) ws += y;
       }
-      const int total = __shfl_sync(0xffffffffu, ws, 31);
+      const int total = __shfl_sync(0xffffffffu, ws, 15);
       const int before = warp ? __shfl_sync(0xffffffffu, ws, warp - 1) : 0;
       const int lo = base + before + x - units;
       if (want >= lo && want < lo + units) {
@@ -322,84 +289,6 @@ __global__ void __launch_bounds__(
     pages = static_cast<int>(all * (blockIdx.z + 1) / gridDim.z - a);
     page0 += static_cast<int>(a);
   }
-  // ---- the first pages, under way while the queries are read
-  auto load_page = [&](int j) {
-    const int rs = j % L::kRaw;
-    const int page = p.c.page_table[static_cast<int64_t>(b) * p.c.max_pages + page0 + j];
-    if (page < 0 || page >= p.c.num_pages) {
-      atomicOr(p.err, kErrBadIndex);
-      mbar_arrive(&raw_full[rs]);
-    } else {
-      mbar_arrive_expect_tx(&raw_full[rs], B::kBytes);
-      bulk_load(smem + L::offRaw + rs * B::kBytes,
-                p.c.cache + (static_cast<int64_t>(page) * p.c.heads + head) * B::kBytes, B::kBytes, &raw_full[rs]);
-    }
-  };
-  if (warp == L::kProducer && lane == 0)
-    for (int j = 0; j < min(pages, L::kRaw); ++j) load_page(j);
-  // ---- queries, scaled by a power of two per row, as fp16 (one part or two): D / 8 lanes to a row, 8 dimensions
-  // each, all warps, the loads of a lane's rows in flight
-  float2* row_q = reinterpret_cast<float2*>(smem + L::offRow);
-  {
-    constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes of a row, rows of a warp at a time
-    constexpr int kStep = L::kThreads / 32 * kAt, kBatch = (kT * kRows + kStep - 1) / kStep;
-    constexpr int kVecs = sizeof(QT) / 2;             // 16-byte loads of 8 dimensions
-    const int c = lane % kLanes;
-    const int t0 = warp * kAt + lane / kLanes;
-    {
-      uint4 raw[kBatch][kVecs];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int row = row0 + t0 + k * kStep;
-        const int i = row / p.G;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            q + (static_cast<int64_t>(q0 + i) * p.Hq + head * p.G + (row - i * p.G)) * D + 8 * c);
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u) raw[k][u] = row < rows && t0 + k * kStep < kT * kRows ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int rr = t0 + k * kStep, tl = rr / kRows, rt = rr % kRows;
-          if (rr >= kT * kRows) break;  // the same for the whole warp
-        const QT* x = reinterpret_cast<const QT*>(raw[k]);
-        float v[8], top = 0.0f;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) {
-          v[d] = static_cast<float>(x[d]);
-          top = fmaxf(top, fabsf(v[d]));
-        }
-#pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int e = pow2_exp(top);
-        const float f = p.sign * pow2(14 - e);
-        // chunk c of the row: dimensions 8c + 0, 4, 1, 5, 2, 6, 3, 7, the order in which a word of codes decodes
-        uint8_t* dst = smem + L::offQ + tl * L::kParts * L::kQPart + (c >> 3) * (kRows * 128) + (rt >> 3) * 1024 +
-                       (rt & 7) * 128 + (((c & 7) ^ (rt & 7)) << 4);
-        float h[8], sum = 0.0f;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) {
-          v[d] *= f;
-          h[d] = __half2float(__float2half_rn(v[d]));
-          sum += h[d];
-        }
-        *reinterpret_cast<uint4*>(dst) =
-            make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
-        if constexpr (kSplit) {
-#pragma unroll
-          for (int d = 0; d < 8; ++d) {
-            h[d] = __half2float(__float2half_rn(v[d] - h[d]));
-            sum += h[d];
-          }
-          *reinterpret_cast<uint4*>(dst + L::kQPart) =
-              make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
-        }
-#pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (c == 0) row_q[rr] = make_float2(sum, p.scale * pow2(e - 14));
-      }
-    }
-    fence_proxy_async_smem();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -409,6 +298,71 @@ __global__ void __launch_bounds__(
     // ------------------------------------------------------------ softmax
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;  // this warp's quarter of the TMEM lanes
     const int tile = warp >> 2;
+    // ---- queries, scaled by a power of two per row, as fp16 (one part or two): D / 8 lanes to a row, 8 dimensions
+    // each, the loads of 8 rows in flight
+    float2* row_q = reinterpret_cast<float2*>(smem + L::offRow);
+    {
+      constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes of a row, rows of a warp at a time
+      constexpr int kStep = 4 * kAt, kBatch = 8;
+      constexpr int kVecs = sizeof(QT) / 2;             // 16-byte loads of 8 dimensions
+      const int c = lane % kLanes;
+#pragma unroll 1
+      for (int t0 = (warp & 3) * kAt + lane / kLanes; t0 < kRows; t0 += kBatch * kStep) {
+        uint4 raw[kBatch][kVecs];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int row = row0 + tile * kRows + t0 + k * kStep;
+          const int i = row / p.G;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              q + (static_cast<int64_t>(q0 + i) * p.Hq + head * p.G + (row - i * p.G)) * D + 8 * c);
+#pragma unroll
+          for (int u = 0; u < kVecs; ++u) raw[k][u] = row < rows ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int rt = t0 + k * kStep;
+          const QT* x = reinterpret_cast<const QT*>(raw[k]);
+          float v[8], top = 0.0f;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            v[d] = static_cast<float>(x[d]);
+            top = fmaxf(top, fabsf(v[d]));
+          }
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int e = pow2_exp(top);
+          const float f = p.sign * pow2(14 - e);
+          // chunk c of the row: dimensions 8c + 0, 4, 1, 5, 2, 6, 3, 7, the order in which a word of codes decodes
+          uint8_t* dst = smem + L::offQ + tile * L::kParts * L::kQPart + (c >> 3) * (kRows * 128) + (rt >> 3) * 1024 +
+                         (rt & 7) * 128 + (((c & 7) ^ (rt & 7)) << 4);
+          float h[8], sum = 0.0f;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            v[d] *= f;
+            h[d] = __half2float(__float2half_rn(v[d]));
+            sum += h[d];
+          }
+          *reinterpret_cast<uint4*>(dst) =
+              make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
+          if constexpr (kSplit) {
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              h[d] = __half2float(__float2half_rn(v[d] - h[d]));
+              sum += h[d];
+            }
+            *reinterpret_cast<uint4*>(dst + L::kQPart) =
+                make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
+          }
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (c == 0) row_q[tile * kRows + rt] = make_float2(sum, p.scale * pow2(e - 14));
+        }
+      }
+      fence_proxy_async_smem();
+    }
+    // the tile's four warps meet: a thread reads its row's factors, which another warp may have written
+    asm volatile("bar.sync %0, 128;" ::"r"(tile + 1) : "memory");
+    if (lane == 0) mbar_arrive(&q_full[tile]);
     const int tile_r0 = row0 + tile * kRows;
     const int r = tile_r0 + (threadIdx.x & 127);  // row of the item
     const bool row_on = r < rows;
@@ -416,7 +370,7 @@ __global__ void __launch_bounds__(
     const int64_t q_at = static_cast<int64_t>(q0 + i_tok) * p.Hq + head * p.G + (row_on ? r - i_tok * p.G : 0);
     const float2 row = row_q[threadIdx.x];
     const float qc = row.y;
-    const f2 qsum2 = f2_pack(row.x, row.x);
+    const f2 qsum2 = f2_pack(row.x, row.x), qc2 = f2_pack(qc, qc);
     const int pos = row_on ? pos0 + i_tok : len - 1;
     const int key_hi = p.causal ? min(pos, len - 1) : len - 1;
     const int key_lo = p.causal && p.window > 0 ? pos - p.window + 1 : 0;
@@ -425,12 +379,12 @@ __global__ void __launch_bounds__(
     const int free_lo = p.causal && p.window > 0 ? pos0 + (min(tile_r0 + kRows, rows) - 1) / p.G - p.window + 1 : 0;
     float m_ref = -INFINITY;
     f2 l2 = 0, z2 = 0;  // sums of the even and of the odd keys
-    int e_run = 0;      // values count up to 2^e_run in O
+    int e_run = 0;
+    bool ok = true;
     // O by f, once the product before page j is done with it.
     auto rescale = [&](int j, float f) -> bool {
       if (!mbar_wait(&pv_done[tile], (j - 1) & 1, p.err, abort_flag)) return false;
       tc_fence_after();
-      __syncwarp();
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         uint32_t o[16];
@@ -442,129 +396,90 @@ __global__ void __launch_bounds__(
       tmem_st_wait();
       return true;
     };
-    // Half hf (32 keys) of a page's scores, as x of p = 2^(c x - ref).
-    auto load_x = [&](uint32_t s_addr, const PageMeta& meta, int hf, f2 (&x)[16]) {
-      uint32_t sv[32];
-      tmem_read_x32(s_addr + 32 * hf, sv);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = f2_pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
-      if constexpr (!kDeq) {
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(&meta.ks[32 * hf + 2 * i]);
-          const ulonglong2 km = *reinterpret_cast<const ulonglong2*>(&meta.kmid[32 * hf + 2 * i]);
-          x[i] = f2_fma(x[i], ks.x, f2_mul(km.x, qsum2));
-          x[i + 1] = f2_fma(x[i + 1], ks.y, f2_mul(km.y, qsum2));
-        }
-      }
-    };
-    // The half's probabilities to W (w0 and, two parts, w1), added to lp and zp.  kMasked: x is -inf where a key is
-    // hidden, whose value row must not matter whatever it holds.
-    auto weigh = [&](const PageMeta& meta, int hf, const f2 (&x)[16], f2 qg2, f2 ref2, float live, f2& lp, f2& zp,
-                     uint32_t* w0, uint32_t* w1, auto masked_tag) {
-      constexpr bool kMasked = decltype(masked_tag)::value;
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        [[maybe_unused]] ulonglong2 vs, vm;
-        if constexpr (!kDeq) {
-          vs = *reinterpret_cast<const ulonglong2*>(&meta.vs[32 * hf + 2 * i]);
-          vm = *reinterpret_cast<const ulonglong2*>(&meta.vmid[32 * hf + 2 * i]);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float wa, wb, xa, xb;
-          f2_unpack(x[i + k], xa, xb);
-          f2_unpack(f2_fma(x[i + k], qg2, ref2), wa, wb);
-          wa = ex2(wa);
-          wb = ex2(wb);
-          if constexpr (kMasked) {
-            if (xa == -INFINITY) wa = 0.0f;
-            if (xb == -INFINITY) wb = 0.0f;
-          }
-          const f2 pr = f2_pack(wa, wb);
-          lp = f2_add(lp, pr);
-          if constexpr (!kDeq) {
-            f2 vmk = k ? vm.y : vm.x;
-            f2_unpack(f2_mul(pr, k ? vs.y : vs.x), wa, wb);
-            if constexpr (kMasked) {
-              float ma, mb;
-              f2_unpack(vmk, ma, mb);
-              if (xa == -INFINITY) wa = ma = 0.0f;
-              if (xb == -INFINITY) wb = mb = 0.0f;
-              vmk = f2_pack(ma, mb);
-            }
-            zp = f2_fma(pr, vmk, zp);
-          }
-          if constexpr (kMasked) {
-            wa *= live;
-            wb *= live;
-          }
-          w0[i + k] = pack_h2(wa, wb);
-          if constexpr (kSplit) {
-            const __half2 h = *reinterpret_cast<const __half2*>(&w0[i + k]);
-            w1[i + k] = pack_h2(wa - __low2float(h), wb - __high2float(h));
-          }
-        }
-      }
-    };
     // A page that every row of the warp sees whole, against the references as they are: no maximum is taken. A row's
     // sum above 2^kLazy (as every probability above it makes) gives the page back to the other path, which moves the
-    // reference; otherwise each probability is within what W holds.
-    auto page_fast = [&](uint32_t s_addr, const PageMeta& meta, int de) -> bool {
-      const float qg = kDeq ? qc * meta.gk : qc, ref = static_cast<float>(de) - m_ref;
-      const f2 qg2 = f2_pack(qg, qg), ref2 = f2_pack(ref, ref);
+    // reference; otherwise each probability is within what W holds.  1: done, 0: not taken, -1: gave up.
+    auto page_fast = [&](int j, uint32_t s_addr, const PageMeta& meta) -> int {
+      const f2 ref2 = f2_pack(-m_ref, -m_ref);
       f2 lp = 0, zp = 0;
       uint32_t w0[32];
       [[maybe_unused]] uint32_t w1[32];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        f2 x[16];
-        load_x(s_addr, meta, hf, x);
-        weigh(meta, hf, x, qg2, ref2, 1.0f, lp, zp, w0 + 16 * hf, w1 + 16 * hf, std::false_type{});
+        uint32_t sv[32];
+        tmem_read_x32(s_addr + 32 * hf, sv);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(&meta.ks[32 * hf + 2 * i]);
+          const ulonglong2 km = *reinterpret_cast<const ulonglong2*>(&meta.kmid[32 * hf + 2 * i]);
+          const ulonglong2 vs = *reinterpret_cast<const ulonglong2*>(&meta.vs[32 * hf + 2 * i]);
+          const ulonglong2 vm = *reinterpret_cast<const ulonglong2*>(&meta.vmid[32 * hf + 2 * i]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const f2 sp = f2_pack(__uint_as_float(sv[2 * (i + k)]), __uint_as_float(sv[2 * (i + k) + 1]));
+            const f2 x = f2_fma(sp, k ? ks.y : ks.x, f2_mul(k ? km.y : km.x, qsum2));
+            float a, b;
+            f2_unpack(f2_fma(x, qc2, ref2), a, b);
+            const f2 pr = f2_pack(ex2(a), ex2(b));
+            lp = f2_add(lp, pr);
+            zp = f2_fma(pr, k ? vm.y : vm.x, zp);
+            float wa, wb;
+            f2_unpack(f2_mul(pr, k ? vs.y : vs.x), wa, wb);
+            const int at = 16 * hf + i + k;
+            w0[at] = pack_h2(wa, wb);
+            if constexpr (kSplit) {
+              const __half2 h = *reinterpret_cast<const __half2*>(&w0[at]);
+              w1[at] = pack_h2(wa - __low2float(h), wb - __high2float(h));
+            }
+          }
+        }
       }
       float a, b;
       f2_unpack(lp, a, b);
-      const float un = pow2(-de);
-      if (__any_sync(0xffffffffu, (a + b) * un > 256.0f)) return false;  // 2^kLazy
-      const f2 un2 = f2_pack(un, un);
-      l2 = f2_fma(lp, un2, l2);
-      z2 = f2_fma(zp, un2, z2);
+      if (__any_sync(0xffffffffu, a + b > 256.0f)) return 0;  // 2^kLazy
+      l2 = f2_add(l2, lp);
+      z2 = f2_add(z2, zp);
+      if (meta.grow && !rescale(j, pow2(-meta.grow))) return -1;
       tmem_st_32x32b_x32(s_addr, w0);
       if constexpr (kSplit) tmem_st_32x32b_x32(s_addr + 32, w1);
-      return true;
+      tmem_st_wait();
+      return 1;
     };
-    // Any page: the maximum first, then the same sums in the same order (a row's bits do not depend on the rows beside
-    // it).  live: 0 where the page's values are too small to count beside those met.
-    auto page = [&](int j, uint32_t s_addr, const PageMeta& meta, int de, float live) -> bool {
-      const float qg = kDeq ? qc * meta.gk : qc;
-      const int hi = meta.ok ? key_hi - meta.key0 : -1, lo = key_lo - meta.key0;
-      auto load_masked = [&](int hf, f2 (&x)[16]) {
-        load_x(s_addr, meta, hf, x);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = 32 * hf + 2 * i;
-          float a, b;
-          f2_unpack(x[i], a, b);
-          if (key > hi || key < lo) a = -INFINITY;
-          if (key + 1 > hi || key + 1 < lo) b = -INFINITY;
-          x[i] = f2_pack(a, b);
-        }
-      };
+    // Any page; kMasked: some key of it is hidden from some row of the tile.
+    auto page = [&](int j, uint32_t s_addr, const PageMeta& meta, auto masked_tag) -> bool {
+      constexpr bool kMasked = decltype(masked_tag)::value;
+      f2 x[32];
       float top = -INFINITY;
-#pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-        f2 x[16];
-        load_masked(hf, x);
+      {
+        uint32_t s0[32], s1[32];
+        tmem_read_x32(s_addr, s0);
+        tmem_read_x32(s_addr + 32, s1);
+        [[maybe_unused]] const int hi = meta.ok ? key_hi - meta.key0 : -1, lo = key_lo - meta.key0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float a, b;
-          f2_unpack(x[i], a, b);
-          top = fmaxf(top, fmaxf(a, b));
+        for (int i = 0; i < 32; i += 2) {
+          const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(&meta.ks[2 * i]);
+          const ulonglong2 km = *reinterpret_cast<const ulonglong2*>(&meta.kmid[2 * i]);
+          const uint32_t* sv = i < 16 ? s0 + 2 * i : s1 + 2 * i - 32;
+          x[i] = f2_fma(f2_pack(__uint_as_float(sv[0]), __uint_as_float(sv[1])), ks.x, f2_mul(km.x, qsum2));
+          x[i + 1] = f2_fma(f2_pack(__uint_as_float(sv[2]), __uint_as_float(sv[3])), ks.y, f2_mul(km.y, qsum2));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float a, b;
+            f2_unpack(x[i + k], a, b);
+            if constexpr (kMasked) {
+              const int key = 2 * (i + k);
+              if (key > hi || key < lo) a = -INFINITY;
+              if (key + 1 > hi || key + 1 < lo) b = -INFINITY;
+              x[i + k] = f2_pack(a, b);
+            }
+            top = fmaxf(top, fmaxf(a, b));
+          }
         }
       }
+      // ---- the reference, and O with it where it moves
       float f = 1.0f;
       if (top != -INFINITY) {
-        const float m = top * qg;
+        const float m = top * qc;
         if (m_ref == -INFINITY) {
           m_ref = m;  // nothing summed yet
         } else if (m > m_ref + kLazy) {
@@ -575,28 +490,59 @@ __global__ void __launch_bounds__(
           z2 = f2_mul(z2, ff);
         }
       }
+      if (meta.grow) f *= pow2(-meta.grow);
       if (j > 0 && __any_sync(0xffffffffu, f != 1.0f) && !rescale(j, f)) return false;
-      const float ref = static_cast<float>(de) - (m_ref == -INFINITY ? 0.0f : m_ref);
-      const f2 qg2 = f2_pack(qg, qg), ref2 = f2_pack(ref, ref);
+      // ---- probabilities, sums, and W over the scores, 32 keys at a time
+      // (the sums in the order of the other path: a row's bits do not depend on the rows beside it)
+      const float ref = m_ref == -INFINITY ? 0.0f : -m_ref;
+      const f2 ref2 = f2_pack(ref, ref);
       f2 lp = 0, zp = 0;
-      // (both halves' W are held back until the scores have been read)
-      uint32_t w0[32];
-      [[maybe_unused]] uint32_t w1[32];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        f2 x[16];
-        load_masked(hf, x);
-        weigh(meta, hf, x, qg2, ref2, live, lp, zp, w0 + 16 * hf, w1 + 16 * hf, std::true_type{});
+        uint32_t w0[16];
+        [[maybe_unused]] uint32_t w1[16];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const ulonglong2 vs = *reinterpret_cast<const ulonglong2*>(&meta.vs[32 * hf + 2 * i]);
+          const ulonglong2 vm = *reinterpret_cast<const ulonglong2*>(&meta.vmid[32 * hf + 2 * i]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const f2 xi = x[16 * hf + i + k];
+            float a, b, wa, wb;
+            f2_unpack(f2_fma(xi, qc2, ref2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            f2 vmk = k ? vm.y : vm.x;
+            f2 pr = f2_pack(a, b), w = f2_mul(pr, k ? vs.y : vs.x);
+            if constexpr (kMasked) {  // whatever the value row of a masked key holds
+              float xa, xb, ma, mb;
+              f2_unpack(xi, xa, xb);
+              f2_unpack(w, wa, wb);
+              f2_unpack(vmk, ma, mb);
+              if (xa == -INFINITY) a = wa = ma = 0.0f;
+              if (xb == -INFINITY) b = wb = mb = 0.0f;
+              pr = f2_pack(a, b);
+              w = f2_pack(wa, wb);
+              vmk = f2_pack(ma, mb);
+            }
+            lp = f2_add(lp, pr);
+            zp = f2_fma(pr, vmk, zp);
+            f2_unpack(w, wa, wb);
+            w0[i + k] = pack_h2(wa, wb);
+            if constexpr (kSplit) {
+              const __half2 h = *reinterpret_cast<const __half2*>(&w0[i + k]);
+              w1[i + k] = pack_h2(wa - __low2float(h), wb - __high2float(h));
+            }
+          }
+        }
+        tmem_st_32x32b_x16(s_addr + 16 * hf, w0);
+        if constexpr (kSplit) tmem_st_32x32b_x16(s_addr + 32 + 16 * hf, w1);
       }
-      const float un = pow2(-de);
-      const f2 un2 = f2_pack(un, un);
-      l2 = f2_fma(lp, un2, l2);
-      z2 = f2_fma(zp, un2, z2);
-      tmem_st_32x32b_x32(s_addr, w0);
-      if constexpr (kSplit) tmem_st_32x32b_x32(s_addr + 32, w1);
+      l2 = f2_add(l2, lp);
+      z2 = f2_add(z2, zp);
+      tmem_st_wait();
       return true;
     };
-    bool ok = true;
     for (int j = 0; j < pages; ++j) {
       const int buf = j & 1, ms = j % L::kMeta;
       const uint32_t s_addr = tmem + lanes + static_cast<uint32_t>(L::s_col(tile, buf));
@@ -608,25 +554,13 @@ __global__ void __launch_bounds__(
       tc_fence_after();
       __syncwarp();
       const PageMeta& meta = metas[ms];
-      // ---- the values' power of two: O moves with it (seldom: it has some room); a page of smaller values is weighed
-      // by 2^de, and not at all beyond 2^-40 (its probabilities still count)
-      const int e = meta.e;
-      if (j == 0) {
-        e_run = e + 1;
-      } else if (e > e_run) {
-        if (!rescale(j, pow2(max(e_run - e - 1, -120)))) {
-          ok = false;
-          break;
-        }
-        e_run = e + 1;
-      }
-      const bool small = e - e_run < -40;
-      const int de = small ? 0 : e - e_run;
+      e_run = meta.e;
       const bool masked = !meta.ok || meta.key0 < free_lo || meta.key0 + kKvPage - 1 > free_hi;
-      const bool fast = !masked && !small && __all_sync(0xffffffffu, m_ref != -INFINITY);
-      if (!fast || !page_fast(s_addr, meta, de)) ok = page(j, s_addr, meta, de, small ? 0.0f : 1.0f);
+      int done = 0;
+      if (!masked && __all_sync(0xffffffffu, m_ref != -INFINITY)) done = page_fast(j, s_addr, meta);
+      ok = done > 0 || (done == 0 && (masked ? page(j, s_addr, meta, std::true_type{})
+                                             : page(j, s_addr, meta, std::false_type{})));
       if (!ok) break;
-      tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -687,173 +621,124 @@ __global__ void __launch_bounds__(
       }
     }
   } else if (warp < L::kProducer) {
-    // ------------------------------------------------------------ decode
-    // Pages first, first + step, .. : their keys and / or values, by kU threads.
-    auto decode_pages = [&](auto threads, auto keys_tag, auto vals_tag, int ut, int first, int step, uint64_t* tab_bar,
-                            PageTab* tabs) {
-      constexpr int kU = decltype(threads)::value;
-      constexpr bool kKeys = decltype(keys_tag)::value, kVals = decltype(vals_tag)::value;
-      constexpr int kWords = D / 8;  // words of a row
-      for (int j = first, it = 0; j < pages; j += step, ++it) {
-        const int rs = j % L::kRaw, ks = j % L::kK, vs = j % L::kV, ms = j % L::kMeta;
-        const int page = p.c.page_table[static_cast<int64_t>(b) * p.c.max_pages + page0 + j];
-        const bool ok = page >= 0 && page < p.c.num_pages;
-        const int key0 = (page0 + j) * kKvPage;
-        if (!mbar_wait(&raw_full[rs], (j / L::kRaw) & 1, p.err, abort_flag)) return;
-        const uint8_t* raw = smem + L::offRaw + rs * B::kBytes;
-        const float2* kmeta = reinterpret_cast<const float2*>(raw + B::offKMeta);
-        const float2* vmeta = reinterpret_cast<const float2*>(raw + B::offVMeta);
-        // ---- factors: every warp finds the page's largest value (value scale), and key where it decodes keys
-        if (!mbar_wait(&meta_empty[ms], ((j / L::kMeta) & 1) ^ 1, p.err, abort_flag)) return;
-        PageMeta& meta = metas[ms];
-        auto largest = [&](const float2* m) {
-          float top = 0.0f;
+    // ------------------------------------------------------------ unpack
+    constexpr int kU = 32 * L::kUnpackWarps;
+    const int ut = threadIdx.x - 32 * L::kSoftWarps;  // 0 .. kU - 1
+    constexpr int kWords = D / 8;                     // words of a row
+    int e_run = -1000;
+    for (int j = 0; j < pages; ++j) {
+      const int rs = j % L::kRaw, ks = j % L::kK, vs = j % L::kV, ms = j % L::kMeta;
+      const int page = p.c.page_table[static_cast<int64_t>(b) * p.c.max_pages + page0 + j];
+      const bool ok = page >= 0 && page < p.c.num_pages;
+      if (!mbar_wait(&raw_full[rs], (j / L::kRaw) & 1, p.err, abort_flag)) break;
+      const uint8_t* raw = smem + L::offRaw + rs * B::kBytes;
+      // ---- keys: a word (8 dimensions) to a 16-byte chunk of the key's operand row.  A thread keeps its word column
+      // and goes down the keys in steps that are multiples of 8, which leave the swizzle as it is.
+      if (!mbar_wait(&k_empty[ks], ((j / L::kK) & 1) ^ 1, p.err, abort_flag)) break;
+      {
+        constexpr int kStep = kU / kWords;  // 8
+        static_assert(kStep % 8 == 0, "the swizzle repeats every 8 rows");
+        const int w = ut % kWords, key = ut / kWords;
+        const uint8_t* src = raw + B::offK + key * B::kRow + 4 * w;
+        uint8_t* dst = smem + L::offK + ks * L::kOp + (w >> 3) * (kKvPage * 128) + (key >> 3) * 1024 + (key & 7) * 128 +
+                       (((w & 7) ^ (key & 7)) << 4);
+        uint32_t a[kKvPage / kStep];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float2 v = m[lane + 32 * i];
-            // bf16: what the row's values lie below, of finite rows
-            const float most = kDeq ? fmaf(8.0f, fabsf(v.x), fabsf(fmaf(8.0f, v.x, v.y))) : v.x;
-            if (ok && key0 + lane + 32 * i < len && (!kDeq || most < INFINITY)) top = fmaxf(top, most);
-          }
-          return pow2_exp(warp_max(top));
-        };
-        // thread ut's row of the page: a key, or a value from thread kKvPage on (where both are decoded)
-        auto factor = [&](const float2* m, bool is_v, int key, int e) {
-          const float2 sm = m[key];
-          const float mid = fmaf(8.0f, sm.x, sm.y);
-          if constexpr (kDeq) {
-            const bool use = ok && key0 + key < len && fmaf(8.0f, fabsf(sm.x), fabsf(mid)) < INFINITY;
-            const float f = pow2(kWExp - e), sc = use ? sm.x * f : 0.0f;
-            const __half hi = __float2half_rn(sc), lo = __float2half_rn(sc - __half2float(hi));
-            const __half md = __float2half_rn(use ? mid * f : 0.0f);
-            PageTab& tab = tabs[it & 1];
-            if (is_v) {
-              tab.v_hi[key] = hi;
-              tab.v_lo[key] = lo;
-              tab.v_mid[key] = md;
-            } else {
-              const uint32_t h2 = __half_as_ushort(hi), l2 = __half_as_ushort(lo), m2 = __half_as_ushort(md);
-              tab.k[key] = make_uint4(h2 | (h2 << 16), l2 | (l2 << 16), m2 | (m2 << 16), 0u);
-            }
-          } else {
-            (is_v ? meta.vs : meta.ks)[key] = is_v ? sm.x * pow2(kWExp - e) : sm.x;
-            (is_v ? meta.vmid : meta.kmid)[key] = mid;
-          }
-        };
-        if constexpr (kKeys) {
-          const int e = kDeq ? largest(kmeta) : 0;
-          if (ut < kKvPage) factor(kmeta, false, ut, e);
-          if (ut == 0) {
-            meta.key0 = key0;
-            meta.ok = ok ? 1 : 0;
-            meta.gk = pow2(e - kWExp);
-          }
+        for (int i = 0; i < kKvPage / kStep; ++i)
+          a[i] = ok ? *reinterpret_cast<const uint32_t*>(src + i * kStep * B::kRow) : 0x88888888u;
+#pragma unroll
+        for (int i = 0; i < kKvPage / kStep; ++i) {
+          const uint32_t a8 = a[i] >> 8;
+          *reinterpret_cast<uint4*>(dst + i * kStep * 128) =
+              make_uint4(codes_lo(a[i]), codes_hi(a[i]), codes_lo(a8), codes_hi(a8));
         }
-        if constexpr (kVals) {
-          const int e = largest(vmeta);
-          const int key = kKeys ? ut - kKvPage : ut;
-          if (key >= 0 && key < kKvPage) factor(vmeta, true, key, e);
-          if (key == 0) meta.e = e;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&meta_full[ms]);
-        if constexpr (kDeq) {  // written by several warps; the other table may still be in use for the page before
-          if (lane == 0) mbar_arrive(&tab_bar[it & 1]);
-          if (!mbar_wait(&tab_bar[it & 1], (it >> 1) & 1, p.err, abort_flag)) return;
-        }
-        // ---- keys: a word (8 dimensions) to a 16-byte chunk of the key's operand row, a thread its word column
-        if constexpr (kKeys) {
-          if (!mbar_wait(&k_empty[ks], ((j / L::kK) & 1) ^ 1, p.err, abort_flag)) return;
-          constexpr int kStep = kU / kWords;
-          const int w = ut % kWords, key = ut / kWords;
-          const uint8_t* src = raw + B::offK + key * B::kRow + 4 * w;
-          uint8_t* dst = smem + L::offK + ks * L::kOp + (w >> 3) * (kKvPage * 128);
-          uint32_t a[kKvPage / kStep];
-#pragma unroll
-          for (int i = 0; i < kKvPage / kStep; ++i)
-            a[i] = ok ? *reinterpret_cast<const uint32_t*>(src + i * kStep * B::kRow) : 0x88888888u;
-#pragma unroll
-          for (int i = 0; i < kKvPage / kStep; ++i) {
-            const int at = key + i * kStep;
-            const uint32_t a8 = a[i] >> 8;
-            uint4 o = make_uint4(codes_lo(a[i]), codes_hi(a[i]), codes_lo(a8), codes_hi(a8));
-            if constexpr (kDeq) {
-              const uint4 f = tabs[it & 1].k[at];
-              o = make_uint4(decode_h2(o.x, f.x, f.y, f.z), decode_h2(o.y, f.x, f.y, f.z), decode_h2(o.z, f.x, f.y, f.z),
-                             decode_h2(o.w, f.x, f.y, f.z));
-            }
-            *reinterpret_cast<uint4*>(dst + at * 128 + (((w & 7) ^ (at & 7)) << 4)) = o;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&k_full[ks]);
-        }
-        // ---- values, transposed: a word of 8 consecutive keys to 8 chunks, one per dimension; dimension 8 w + d is
-        // operand row d (D / 8) + w, so that a warp's chunks of one d lie in consecutive rows (different banks)
-        if constexpr (kVals) {
-          if (!mbar_wait(&v_empty[vs], ((j / L::kV) & 1) ^ 1, p.err, abort_flag)) return;
-          static_assert(8 * kWords % kU == 0, "whole turns of the group");
-#pragma unroll 1
-          for (int id = ut; id < 8 * kWords; id += kU) {
-            const int w = id % kWords, kg = id / kWords;
-            const uint8_t* src = raw + B::offV + 8 * kg * B::kRow + 4 * w;
-            uint8_t* dst = smem + L::offV + vs * L::kOp + (w >> 3) * 1024 + (w & 7) * 128 + ((kg ^ (w & 7)) << 4);
-            uint32_t a[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) a[k] = ok ? *reinterpret_cast<const uint32_t*>(src + k * B::kRow) : 0x88888888u;
-            [[maybe_unused]] uint4 fh, fl, fm;
-            if constexpr (kDeq) {  // of the 8 keys, neighbours in the halves of a word
-              fh = reinterpret_cast<const uint4*>(tabs[it & 1].v_hi)[kg];
-              fl = reinterpret_cast<const uint4*>(tabs[it & 1].v_lo)[kg];
-              fm = reinterpret_cast<const uint4*>(tabs[it & 1].v_mid)[kg];
-            }
-            auto put = [&](uint8_t* at, uint4 o) {
-              if constexpr (kDeq)
-                o = make_uint4(decode_h2(o.x, fh.x, fl.x, fm.x), decode_h2(o.y, fh.y, fl.y, fm.y),
-                               decode_h2(o.z, fh.z, fl.z, fm.z), decode_h2(o.w, fh.w, fl.w, fm.w));
-              *reinterpret_cast<uint4*>(at) = o;
-            };
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t sel = c | ((4 + c) << 8);
-              uint32_t pr[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) pr[k] = prmt_b32(a[2 * k], a[2 * k + 1], sel);
-              put(dst + 2 * c * kWords * 128,
-                  make_uint4(codes_lo(pr[0]), codes_lo(pr[1]), codes_lo(pr[2]), codes_lo(pr[3])));
-              put(dst + (2 * c + 1) * kWords * 128,
-                  make_uint4(codes_hi(pr[0]), codes_hi(pr[1]), codes_hi(pr[2]), codes_hi(pr[3])));
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&v_full[vs]);
-        }
-        if (lane == 0) mbar_arrive(&raw_empty[rs]);
       }
-    };
-    using Yes = std::true_type;
-    using No = std::false_type;
-    const int uw = warp - L::kSoftWarps, ut = threadIdx.x - 32 * L::kSoftWarps;
-    PageTab* tabs = reinterpret_cast<PageTab*>(smem + L::offTab);
-    if constexpr (L::kByRole) {
-      if (uw < L::kKeyWarps)
-        decode_pages(std::integral_constant<int, 32 * L::kKeyWarps>{}, Yes{}, No{}, ut, 0, 1, tab_full, tabs);
-      else
-        decode_pages(std::integral_constant<int, 32 * L::kValWarps>{}, No{}, Yes{}, ut - 32 * L::kKeyWarps, 0, 1,
-                     tab_full + 2, tabs);
-    } else {
-      const int group = uw >> 2;
-      decode_pages(std::integral_constant<int, 128>{}, Yes{}, Yes{}, ut - 128 * group, group, L::kGroups,
-                   tab_full + 2 * group, tabs + 2 * group);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full[ks]);
+      // ---- factors
+      if (!mbar_wait(&meta_empty[ms], ((j / L::kMeta) & 1) ^ 1, p.err, abort_flag)) break;
+      {
+        // every warp needs the page's largest value scale (of tokens that exist)
+        const float2* vmeta = reinterpret_cast<const float2*>(raw + B::offVMeta);
+        const int key0 = (page0 + j) * kKvPage;
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (ok && key0 + lane + 32 * i < len) top = fmaxf(top, vmeta[lane + 32 * i].x);
+        top = warp_max(top);
+        const int e_pg = pow2_exp(top);
+        int grow = 0;
+        if (e_run == -1000) {
+          e_run = e_pg + 1;  // some room, so that it seldom moves
+        } else if (e_pg > e_run) {
+          grow = e_pg + 1 - e_run;
+          e_run = e_pg + 1;
+        }
+        PageMeta& meta = metas[ms];
+        if (ut < 2 * kKvPage) {
+          const bool is_v = ut >= kKvPage;
+          const int key = ut & (kKvPage - 1);
+          const float2 sm = reinterpret_cast<const float2*>(raw + (is_v ? B::offVMeta : B::offKMeta))[key];
+          const float mid = fmaf(8.0f, sm.x, sm.y);
+          (is_v ? meta.vs : meta.ks)[key] = is_v ? sm.x * pow2(kWExp - e_run) : sm.x;
+          (is_v ? meta.vmid : meta.kmid)[key] = mid;
+        }
+        if (ut == 0) {
+          meta.key0 = key0;
+          meta.ok = ok ? 1 : 0;
+          meta.grow = grow;
+          meta.e = e_run;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&meta_full[ms]);
+      // ---- values, transposed: a word of 8 consecutive keys to 8 chunks, one per dimension; dimension 8 w + d is
+      // operand row d (D / 8) + w, so that a warp's chunks of one d lie in consecutive rows (different banks)
+      if (!mbar_wait(&v_empty[vs], ((j / L::kV) & 1) ^ 1, p.err, abort_flag)) break;
+      {
+        static_assert(8 * kWords == kU, "a thread takes one word of 8 keys");
+        const int w = ut % kWords, kg = ut / kWords;
+        const uint8_t* src = raw + B::offV + 8 * kg * B::kRow + 4 * w;
+        uint8_t* dst = smem + L::offV + vs * L::kOp + (w >> 3) * 1024 + (w & 7) * 128 + ((kg ^ (w & 7)) << 4);
+        uint32_t a[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k] = ok ? *reinterpret_cast<const uint32_t*>(src + k * B::kRow) : 0x88888888u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t sel = c | ((4 + c) << 8);
+          uint32_t pr[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) pr[k] = prmt_b32(a[2 * k], a[2 * k + 1], sel);
+          *reinterpret_cast<uint4*>(dst + 2 * c * kWords * 128) =
+              make_uint4(codes_lo(pr[0]), codes_lo(pr[1]), codes_lo(pr[2]), codes_lo(pr[3]));
+          *reinterpret_cast<uint4*>(dst + (2 * c + 1) * kWords * 128) =
+              make_uint4(codes_hi(pr[0]), codes_hi(pr[1]), codes_hi(pr[2]), codes_hi(pr[3]));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&v_full[vs]);
+        mbar_arrive(&raw_empty[rs]);
+      }
     }
   } else if (warp == L::kProducer) {
     // ------------------------------------------------------------ raw pages
     if (lane == 0) {
-      int j = min(pages, L::kRaw);
+      int j = 0;
       for (; j < pages; ++j) {
-        if (!mbar_wait(&raw_empty[j % L::kRaw], ((j / L::kRaw) & 1) ^ 1, p.err, abort_flag)) break;
-        load_page(j);
+        const int rs = j % L::kRaw;
+        const int page = p.c.page_table[static_cast<int64_t>(b) * p.c.max_pages + page0 + j];
+        if (!mbar_wait(&raw_empty[rs], ((j / L::kRaw) & 1) ^ 1, p.err, abort_flag)) break;
+        if (page < 0 || page >= p.c.num_pages) {
+          atomicOr(p.err, kErrBadIndex);
+          mbar_arrive(&raw_full[rs]);
+        } else {
+          mbar_arrive_expect_tx(&raw_full[rs], B::kBytes);
+          bulk_load(smem + L::offRaw + rs * B::kBytes,
+                    p.c.cache + (static_cast<int64_t>(page) * p.c.heads + head) * B::kBytes, B::kBytes, &raw_full[rs]);
+        }
       }
       if (*abort_flag)  // given up: copies still in flight must land before the CTA's shared memory goes
         for (int i = max(0, j - L::kRaw); i < j; ++i) mbar_wait(&raw_full[i % L::kRaw], (i / L::kRaw) & 1, p.err);
@@ -882,7 +767,7 @@ __global__ void __launch_bounds__(
         tc_commit(&k_empty[ks]);
         return true;
       };
-      bool ok = pages == 0 || scores(0);
+      bool ok = pages == 0 || (mbar_wait(&q_full[t], 0, p.err, abort_flag) && scores(0));
       for (int j = 0; ok && j < pages; ++j) {
         if (j + 1 < pages) {
           // the other score buffer holds W of the page before: its product must be done with it
@@ -966,7 +851,8 @@ __global__ void __launch_bounds__(128) k_kv4_join_rows(const Problem p, int spli
 
 template <int D, typename QT, typename OT>
 cudaError_t launch_t(DeviceContext* ctx, Problem p, const void* q, void* out, cudaStream_t s, int* status) {
-  using L = Layout<D, std::is_same<QT, float>::value, std::is_same<QT, __nv_bfloat16>::value>;
+  constexpr bool kSplit = std::is_same<QT, float>::value;
+  using L = Layout<D, kSplit>;
   // units of kT * 128 rows: any division of T rows into sequences of at most max_q has at most this many
   const int64_t per = L::kT * kRows;
   const int64_t units = static_cast<int64_t>(p.T) * p.G / per + (p.c.num_seqs < p.T ? p.c.num_seqs : p.T);
@@ -986,7 +872,7 @@ cudaError_t launch_t(DeviceContext* ctx, Problem p, const void* q, void* out, cu
     if ((*status = pool_alloc(ctx, reinterpret_cast<void**>(&ws), bytes, s))) return cudaSuccess;
     p.part = reinterpret_cast<float*>(ws);
   }
-  auto kern = k_kv4_prefill<D, QT, OT>;
+  auto kern = k_kv4_prefill<D, kSplit, QT, OT>;
   cudaError_t e = allow_smem(ctx, reinterpret_cast<const void*>(kern), L::kAlloc);
   if (e == cudaSuccess) {
     kern<<<dim3(static_cast<unsigned>(units * p.c.heads), 1, static_cast<unsigned>(splits)), L::kThreads, L::kAlloc, s>>>(

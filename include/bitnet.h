@@ -408,12 +408,10 @@ BITNET_API int bitnet_kv4_read(const bitnet_kv4* c, int64_t T, void* k, void* v,
  * all of them when causal is 0 (window must then be 0).  A row that sees no key
  * gives zeros.  max_q_len: an upper bound of the sequences' row counts; rows of
  * a longer sequence are recorded as BITNET_ERR_BAD_INDEX and may be left out.
- * q in q_dtype, out in the same type or in BITNET_DTYPE_F32.  Scores, softmax
- * and sums are fp32.  fp32 queries and their probabilities enter the products
- * with 22 bits, and the cache's codes exactly.  16-bit queries enter exactly;
- * their probabilities may be rounded to fp16's 11 bits, and with bf16 queries
- * and more than a few rows per sequence so may the keys and values that the
- * cache stands for.  scale finite. */
+ * q in q_dtype, out in the same type or in BITNET_DTYPE_F32; sums, softmax and
+ * scores are fp32, products of q and of the probabilities with the cache's
+ * integer codes exact up to 2^-22 (q or probability; 16-bit q: the
+ * probabilities may be rounded to 2^-11).  scale finite. */
 BITNET_API int bitnet_kv4_attention(const bitnet_kv4* c, const void* q, int q_dtype, int64_t T, int32_t num_heads,
                                     int32_t max_q_len, float scale, int causal, int32_t window, void* out,
                                     int out_dtype, bitnet_stream_t stream);

@@ -78,25 +78,13 @@ class Case:
         self.kc, self.vc, self.km, self.vm = kc, vc, km, vm
         self.cache = make_block_bytes(kc, vc, km, vm)
 
-    def kv(self, b, fp16=False):
-        """(K, V) [Hkv, len, D] in float64 of sequence b, and the scales [2, Hkv, len]; fp16: as the 16-bit operands
-        that bf16 queries of many rows meet, (c - 8) s + (m + 8 s) in two roundings with s in two parts, scaled so that
-        a page's largest row is in fp16's range."""
+    def kv(self, b):
+        """(K, V) [Hkv, len, D] in float64 of sequence b, and the scales [2, Hkv, len]."""
         n = self.lens[b]
         pg = self.table[b, :(n + PAGE - 1) // PAGE]
         out, sc = [], []
         for c, m in ((self.kc, self.km), (self.vc, self.vm)):
             x = c[pg].astype(np.float64) * m[pg][..., :1] + m[pg][..., 1:]
-            if fp16:
-                s, lo = np.nan_to_num(m[pg][..., :1]), np.nan_to_num(m[pg][..., 1:])
-                mid = (np.float32(8) * s + lo).astype(np.float32)
-                top = (8 * np.abs(s) + np.abs(mid)).max((2, 3), keepdims=True)
-                f = 2.0 ** (6 - np.floor(np.log2(np.maximum(top, 1e-30))))
-                hi = (s * f).astype(np.float16)
-                rest = (s * f - hi).astype(np.float16)
-                d = c[pg].astype(np.float64) - 8
-                t = (d * rest + (mid * f).astype(np.float16)).astype(np.float16)
-                x = (d * hi + t).astype(np.float16).astype(np.float64) / f
             out.append(x.transpose(1, 0, 2, 3).reshape(self.Hkv, -1, self.D)[:, :n])
             sc.append(m[pg][..., 0].transpose(1, 0, 2).reshape(self.Hkv, -1)[:, :n])
         return out[0], out[1], np.stack(sc)
@@ -107,7 +95,7 @@ class Case:
                     page_table=t(self.table))
 
 
-def attention(case, q, scale, causal=True, window=0, skip_pages=(), fp16=False):
+def attention(case, q, scale, causal=True, window=0, skip_pages=()):
     """(out, bound) float64 [T, Hq, D]: the definition, and how far a kernel's fp32 result may be from it.
 
     Bound: the score of a key is a sum of D products formed from exact integer codes in fp32 (at most 2 D / 16 + 8
@@ -123,7 +111,7 @@ def attention(case, q, scale, causal=True, window=0, skip_pages=(), fp16=False):
         L = case.lens[b]
         if n == 0 or L == 0:
             continue
-        K, V, sc = case.kv(b, fp16)
+        K, V, sc = case.kv(b)
         pos = np.arange(L - n, L)[:, None]
         j = np.arange(L)[None, :]
         see = np.ones((n, L), bool)
@@ -150,33 +138,9 @@ def attention(case, q, scale, causal=True, window=0, skip_pages=(), fp16=False):
             vmax = np.abs(vv).max()
             s = sc[1][h // G].max()
             bound[t0:t0 + n, h] = 2 * e * vmax + (L / 8 + 64) * 2.0 ** -24 * (vmax + 15 * s)
-            # what a rounded probability multiplies: half a row's range around its middle, or (fp16) the whole value;
-            # operands far below their page's largest row are fp16 subnormals, off by 2^-25 where that row is above 2^5
-            case.half_range = max(getattr(case, "half_range", 0.0), vmax if fp16 else 8 * s)
-            if fp16:
-                bound[t0:t0 + n, h] += 2.0 ** -29 * (vmax + 2 * vmax * abs(scale) * np.abs(qq).sum(1, keepdims=True)
-                                                     * np.abs(kk).max())
+            case_s = 7.5 * s  # half a row's range: what a rounded probability multiplies
+            case.half_range = max(getattr(case, "half_range", 0.0), case_s)
     return out, bound
-
-
-def rounding_bound(case, q, scale):
-    """How far rounding the keys and values to fp16 moves the output of each row [T, Hq, 1], from the definition alone:
-    each value is off by at most 2^-11 of itself and of its row's middle (two roundings of half a step), so a score by
-    d <= |scale| |q| 2^-11 (|k| + sqrt(D) |mid|) (Cauchy-Schwarz), a probability by a factor of 1 +- 2 d, and the output
-    by 2 d max|v| + 2^-11 2 max|v|."""
-    out = np.zeros((case.T, q.shape[1], 1))
-    G = q.shape[1] // case.Hkv
-    for b, n in enumerate(case.counts):
-        if n == 0 or case.lens[b] == 0:
-            continue
-        K, V, _ = case.kv(b)
-        t0 = int(case.q_start[b])
-        for h in range(q.shape[1]):
-            kk, vmax = K[h // G], np.abs(V[h // G]).max()
-            size = (np.linalg.norm(kk, axis=1) + case.D ** 0.5 * np.abs(kk).max(1)).max()
-            d = abs(scale) * np.linalg.norm(q[t0:t0 + n, h].astype(np.float64), axis=1) * 2.0 ** -11 * size
-            out[t0:t0 + n, h, 0] = (np.exp(2 * np.minimum(d, 50)) - 1) * vmax + 2.0 ** -10 * vmax
-    return out
 
 
 def bound_for(case, ref, bound, q_dtype, out_dtype):
