@@ -6,13 +6,21 @@
 // quotient.  The quotient is formed in fp32 as (x - min) * (15 / (max - min)),
 // whose error is below 4 * 2^-24 * 15 < 4e-6 (one rounding each of the
 // difference, the range, its reciprocal and the product); where it lies within
-// 1e-5 of the border between two codes the code is decided in double instead
-// (about one value in 50 000), so that it never depends on that rounding.
+// 1e-5 of the border between two codes the code is decided by exact fp32
+// arithmetic, or in double where that is not exact, so that it never depends on
+// that rounding.
 // A row with max - min < 1e-30 (a constant row) has scale 0 and codes 0.
 //
-// D / 16 lanes share a row, 16 values each: two or four 16-byte loads per lane,
-// a min/max exchange over the row's lanes, one 8-byte store of codes.  Bound by
-// memory for many rows, by one row's latency for few.
+// Append: D / 16 lanes share a row, 16 values each: two or four 16-byte loads per
+// lane, a min/max exchange over the row's lanes, one 8-byte store of codes; a warp
+// holds the keys and values of 512 / D heads, so that it looks its place up once.
+// 32768 rows of 8 heads of 128, written and read back: bf16 68 us and 35 us (2.5
+// and 4.9 TB/s), fp32 56 us and 55 us (5.5 TB/s).  Reading and writing fp32 are
+// bound by memory; bf16 by instruction issue (0.61 per cycle and scheduler): 20
+// per value to quantise, and about every row of bf16 values has one on a border.
+// All values of such a lane decided in double took 1195 us, in exact fp32 87 us,
+// only those on a border 68 us.  A few rows are bound by the latency of the place's
+// lookup (sequence, length, page), behind which the row's own loads hide.
 #include <type_traits>
 
 #include "common.cuh"
@@ -25,12 +33,81 @@ namespace {
 
 constexpr int kWarps = 8;
 
-__device__ __forceinline__ int quant_code(float x, float lo, float hi, float inv) {
-  const float t = __fmul_rn(__fsub_rn(x, lo), inv);
-  float r = rintf(t);
-  if (fabsf(fabsf(t - r) - 0.5f) < 1e-5f)
-    r = static_cast<float>(rint((static_cast<double>(x) - lo) * 15.0 / (static_cast<double>(hi) - lo)));
-  return static_cast<int>(fminf(fmaxf(r, 0.0f), 15.0f));
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Distance of a quotient from its rounded value above which its side of the
+// border is not certain.
+constexpr float kNear = 0.49999f;
+
+// The quotient 15 (x - lo) / (hi - lo) in fp32: the same operations as quant8's.
+__device__ __forceinline__ float quotient(float x, float lo, float inv) { return __fmul_rn(__fsub_rn(x, lo), inv); }
+
+// Eight codes round(15 (x - lo) / (hi - lo)) as 32 bits, lowest first, two at a
+// time by paired operations.  `near` keeps the largest distance of a quotient
+// from its rounded value.  The codes are packed by fp32 multiply-adds (exact:
+// four codes are below 2^16), even and odd ones side by side.
+__device__ __forceinline__ uint32_t quant8(const float* x, float lo, float inv, float& near) {
+  const uint64_t lo2 = pair(-lo, -lo), inv2 = pair(inv, inv), magic = pair(kRoundMagic, kRoundMagic);
+  const uint64_t less = pair(-kRoundMagic, -kRoundMagic), minus = pair(-1.0f, -1.0f), step = pair(256.0f, 256.0f);
+  uint32_t half[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint64_t r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t t = mul2(add2(pair(x[4 * h + 2 * i], x[4 * h + 2 * i + 1]), lo2), inv2);
+      r[i] = add2(add2(t, magic), less);  // rint(t), t in [0, 15]
+      const float2 d = unpair(fma2(r[i], minus, t));
+      near = fmaxf(near, fmaxf(fabsf(d.x), fabsf(d.y)));
+    }
+    const float2 p = unpair(fma2(r[1], step, r[0]));  // codes 0, 2 and 1, 3
+    half[h] = __float_as_uint(__fadd_rn(__fmaf_rn(p.y, 16.0f, p.x), 8388608.0f));  // 2^23 + the four
+  }
+  return __byte_perm(half[0], half[1], 0x5410);
+}
+
+// The code of a value whose quotient lies next to a border.  With k = rint(t) it
+// is k, or its neighbour towards the residual r = 15 (x - lo) - k (hi - lo) when
+// 2 |r| > hi - lo, or = and k is odd.  16-bit inputs often sit exactly on a border
+// (about one value of a row of 128 bf16 normals), and their differences and
+// products are mostly exact in fp32, which decides; where one is not, double does.
+__device__ __forceinline__ uint32_t border_code(float x, float lo, float hi, float span, float inv) {
+  const float d = __fsub_rn(x, lo);
+  float k = rintf(__fmul_rn(d, inv));
+  const float q = __fmul_rn(15.0f, d), p = __fmul_rn(k, span), r = __fsub_rn(q, p);
+  const bool exact = __fadd_rn(span, lo) == hi && __fadd_rn(d, lo) == x && __fmaf_rn(15.0f, d, -q) == 0.0f &&
+                     __fmaf_rn(k, span, -p) == 0.0f && __fadd_rn(r, p) == q;
+  if (exact) {
+    const float r2 = __fmul_rn(2.0f, fabsf(r));
+    if (r2 > span || (r2 == span && (static_cast<int>(k) & 1))) k += copysignf(1.0f, r);
+  } else {
+    k = static_cast<float>(rint((static_cast<double>(x) - lo) * 15.0 / (static_cast<double>(hi) - lo)));
+  }
+  return static_cast<uint32_t>(fminf(fmaxf(k, 0.0f), 15.0f));
 }
 
 // Where row `row` of the plan (token * heads + head) lives in the cache, or
@@ -54,98 +131,168 @@ __device__ __forceinline__ uint8_t* locate(const KvView& c, int t, int head, int
   return p;
 }
 
-// A warp takes 512 / D heads of one token's keys or values (blockIdx.y: keys,
-// values).
-template <int D, typename T, bool kRead>
-__global__ void __launch_bounds__(kWarps * 32) k_kv4_rows(KvView c, T* __restrict__ k, T* __restrict__ v, int T_rows,
-                                                          unsigned* err) {
+// 16 values to a lane's part of a row: codes (8 bytes) and the row's scale and
+// minimum, exchanged between the row's kLanes lanes.
+template <int kLanes>
+__device__ __forceinline__ uint2 quantise_row(const float (&f)[16], float2& meta) {
+  float lo = f[0], hi = f[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) {
+    lo = fminf(lo, f[i]);
+    hi = fmaxf(hi, f[i]);
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  const float span = __fsub_rn(hi, lo);
+  const bool flat = span < 1e-30f;
+  meta = make_float2(flat ? 0.0f : __fdiv_rn(span, 15.0f), lo);
+  if (flat) return make_uint2(0u, 0u);
+  const float inv = __fdiv_rn(15.0f, span);
+  float near = 0.0f;
+  uint2 w;
+  w.x = quant8(f, lo, inv, near);
+  w.y = quant8(f + 8, lo, inv, near);
+  if (!(near < kNear)) {
+    unsigned todo = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float t = quotient(f[i], lo, inv);
+      const float r = __fsub_rn(__fadd_rn(t, kRoundMagic), kRoundMagic);
+      if (!(fabsf(__fsub_rn(t, r)) < kNear)) todo |= 1u << i;
+    }
+    while (todo) {  // mostly one
+      const int i = __ffs(todo) - 1;
+      todo &= todo - 1;
+      float x = f[0];
+#pragma unroll
+      for (int j = 1; j < 16; ++j) x = i == j ? f[j] : x;
+      const uint32_t code = border_code(x, lo, hi, span, inv), at = 4 * (i & 7), keep = ~(15u << at);
+      if (i < 8) w.x = (w.x & keep) | code << at;
+      else w.y = (w.y & keep) | code << at;
+    }
+  }
+  return w;
+}
+
+template <typename T>
+__device__ __forceinline__ void load16(const T* x, float (&f)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 q = load4(x + 4 * i);
+    f[4 * i] = q.x;
+    f[4 * i + 1] = q.y;
+    f[4 * i + 2] = q.z;
+    f[4 * i + 3] = q.w;
+  }
+}
+
+// The values of kPer = 4 or 8 codes (low bits of `word`), to x: one 16-byte store.
+template <typename T>
+__device__ __forceinline__ void store_values(T* x, uint32_t word, float2 meta) {
+  constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+  union { T v[kPer]; uint4 u; } o;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    // 2^23 + code, less 2^23: an integer in float without the conversion unit
+    const float c = __fsub_rn(__uint_as_float(((word >> (4 * i)) & 15u) | 0x4b000000u), 8388608.0f);
+    o.v[i] = round_out<T>(__fadd_rn(__fmul_rn(c, meta.x), meta.y));
+  }
+  *reinterpret_cast<uint4*>(x) = o.u;
+}
+
+// A warp takes the keys and the values of 512 / D heads of one token.  What it
+// writes depends on a chain of small loads (sequence, length, page): the rows'
+// own loads are issued before it.
+template <int D, typename T>
+__global__ void __launch_bounds__(kWarps * 32) k_kv4_append(KvView c, const T* __restrict__ k, const T* __restrict__ v,
+                                                            int T_rows, unsigned* err) {
   constexpr int kLanes = D / 16;       // lanes per row
   constexpr int kRows = 32 / kLanes;   // rows per warp
   using B = KvBlock<D>;
-  pdl_wait();
-  pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int groups = (c.heads + kRows - 1) / kRows;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int t = static_cast<int>(w / groups);
   if (t >= T_rows) return;
-  const int head = static_cast<int>(w % groups) * kRows + lane / kLanes;
+  const int head = static_cast<int>(w - static_cast<int64_t>(t) * groups) * kRows + lane / kLanes;
   const bool on = head < c.heads;
   const int l = lane % kLanes;
+  const int64_t at = (static_cast<int64_t>(t) * c.heads + (on ? head : 0)) * D + 16 * l;
+  float fk[16], fv[16];
+  load16(k + at, fk);
+  load16(v + at, fv);
   int slot = 0;
   uint8_t* blk = locate<D>(c, t, on ? head : 0, lane, &slot, err);
   if (!blk) return;  // the same for all lanes
-  const bool is_v = blockIdx.y != 0;
-  T* x = (is_v ? v : k) + (static_cast<int64_t>(t) * c.heads + (on ? head : 0)) * D + 16 * l;
-  uint2* codes = reinterpret_cast<uint2*>(blk + (is_v ? B::offV : B::offK) + slot * B::kRow + 8 * l);
-  float2* meta = reinterpret_cast<float2*>(blk + (is_v ? B::offVMeta : B::offKMeta) + slot * 8);
-  if constexpr (kRead) {
-    if (!on) return;
-    const uint2 w2 = *codes;
-    const float2 sm = *meta;
-    float f[16];
+  uint2* kc = reinterpret_cast<uint2*>(blk + B::offK + slot * B::kRow + 8 * l);
+  uint2* vc = reinterpret_cast<uint2*>(blk + B::offV + slot * B::kRow + 8 * l);
+  float2* km = reinterpret_cast<float2*>(blk + B::offKMeta + slot * 8);
+  float2* vm = reinterpret_cast<float2*>(blk + B::offVMeta + slot * 8);
+  float2 ma, mb;
+  const uint2 a = quantise_row<kLanes>(fk, ma), b = quantise_row<kLanes>(fv, mb);
+  if (!on) return;
+  *kc = a;
+  *vc = b;
+  if (l == 0) {
+    *km = ma;
+    *vm = mb;
+  }
+}
+
+// The inverse, 8 heads of a token to a warp: every store instruction covers 512
+// consecutive bytes of values.
+template <int D, typename T>
+__global__ void __launch_bounds__(kWarps * 32) k_kv4_read(KvView c, T* __restrict__ k, T* __restrict__ v, int T_rows,
+                                                          unsigned* err) {
+  constexpr int kPer = 16 / static_cast<int>(sizeof(T));    // values of a store
+  constexpr int kLanes = D / kPer < 32 ? D / kPer : 32;     // lanes of a row
+  constexpr int kTurns = D / (kPer * kLanes);               // stores of a row
+  constexpr int kAt = 32 / kLanes, kHeads = 8;              // rows at a time, heads of a warp
+  using B = KvBlock<D>;
+  const int lane = threadIdx.x & 31;
+  const int groups = (c.heads + kHeads - 1) / kHeads;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int t = static_cast<int>(w / groups);
+  if (t >= T_rows) return;
+  const int head0 = static_cast<int>(w - static_cast<int64_t>(t) * groups) * kHeads;
+  int slot = 0;
+  const uint8_t* blk0 = locate<D>(c, t, head0, lane, &slot, err);
+  if (!blk0) return;
+  const int l = lane % kLanes;
+#pragma unroll 4
+  for (int h = lane / kLanes; h < kHeads; h += kAt) {
+    if (head0 + h >= c.heads) break;
+    const uint8_t* blk = blk0 + static_cast<int64_t>(h) * B::kBytes;
+    const int64_t at = (static_cast<int64_t>(t) * c.heads + head0 + h) * D;
+    const float2 ma = *reinterpret_cast<const float2*>(blk + B::offKMeta + slot * 8);
+    const float2 mb = *reinterpret_cast<const float2*>(blk + B::offVMeta + slot * 8);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t word = i < 8 ? w2.x : w2.y;
-      f[i] = __fadd_rn(__fmul_rn(static_cast<float>((word >> (4 * (i & 7))) & 15u), sm.x), sm.y);
+    for (int i = 0; i < kTurns; ++i) {
+      const int d = kPer * (l + kLanes * i);
+      const uint8_t* kc = blk + B::offK + slot * B::kRow + d / 2;
+      const uint8_t* vc = blk + B::offV + slot * B::kRow + d / 2;
+      const uint32_t a = kPer == 4 ? *reinterpret_cast<const uint16_t*>(kc) : *reinterpret_cast<const uint32_t*>(kc);
+      const uint32_t b = kPer == 4 ? *reinterpret_cast<const uint16_t*>(vc) : *reinterpret_cast<const uint32_t*>(vc);
+      store_values(k + at + d, a, ma);
+      store_values(v + at + d, b, mb);
     }
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        reinterpret_cast<float4*>(x)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-    } else {
-      union { T h[16]; uint4 u[2]; } o;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o.h[i] = round_out<T>(f[i]);
-      reinterpret_cast<uint4*>(x)[0] = o.u[0];
-      reinterpret_cast<uint4*>(x)[1] = o.u[1];
-    }
-  } else {
-    float f[16];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 q = load4(x + 4 * i);
-      f[4 * i] = q.x;
-      f[4 * i + 1] = q.y;
-      f[4 * i + 2] = q.z;
-      f[4 * i + 3] = q.w;
-    }
-    float lo = f[0], hi = f[0];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) {
-      lo = fminf(lo, f[i]);
-      hi = fmaxf(hi, f[i]);
-    }
-#pragma unroll
-    for (int o = kLanes / 2; o; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    if (!on) return;
-    const float span = __fsub_rn(hi, lo);
-    const bool flat = span < 1e-30f;
-    const float scale = flat ? 0.0f : __fdiv_rn(span, 15.0f);
-    const float inv = flat ? 0.0f : __fdiv_rn(15.0f, span);
-    uint2 w2 = make_uint2(0u, 0u);
-    if (!flat) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        w2.x |= static_cast<uint32_t>(quant_code(f[i], lo, hi, inv)) << (4 * i);
-        w2.y |= static_cast<uint32_t>(quant_code(f[8 + i], lo, hi, inv)) << (4 * i);
-      }
-    }
-    *codes = w2;
-    if (l == 0) *meta = make_float2(scale, lo);
   }
 }
 
 template <int D, typename T, bool kRead>
 cudaError_t launch_rows(const DeviceContext* ctx, const KvView& c, void* k, void* v, int64_t T_rows, cudaStream_t s) {
-  const int64_t groups = (c.heads + 512 / D - 1) / (512 / D);
+  constexpr int kHeads = kRead ? 8 : 512 / D;  // of a warp
+  const int64_t groups = (c.heads + kHeads - 1) / kHeads;
   const int64_t ctas = (T_rows * groups + kWarps - 1) / kWarps;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  k_kv4_rows<D, T, kRead><<<dim3(static_cast<unsigned>(ctas), 2), kWarps * 32, 0, s>>>(
-      c, static_cast<T*>(k), static_cast<T*>(v), static_cast<int>(T_rows), ctx->err_word);
+  const unsigned grid = static_cast<unsigned>(ctas);
+  const int rows = static_cast<int>(T_rows);
+  T *kp = static_cast<T*>(k), *vp = static_cast<T*>(v);
+  if constexpr (kRead) k_kv4_read<D, T><<<grid, kWarps * 32, 0, s>>>(c, kp, vp, rows, ctx->err_word);
+  else k_kv4_append<D, T><<<grid, kWarps * 32, 0, s>>>(c, kp, vp, rows, ctx->err_word);
   return cudaGetLastError();
 }
 

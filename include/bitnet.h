@@ -363,8 +363,8 @@ BITNET_API int bitnet_w8a8_forward(const void* x, int x_dtype, const float* norm
  * holds of it, so row i of its n rows is position kv_lens[b] - n + i.  Position j
  * lies in page page_table[b * max_pages + j / 64], slot j % 64.  Rows before
  * q_start[0] and from q_start[num_seqs] on belong to no sequence, and rows of
- * negative position to no token: they are neither read nor written (their
- * attention output, for the latter, is 0).  Page-table entries of positions
+ * negative position to no token: nothing is written for them and
+ * their values change nothing (the attention output of the latter is 0).  Page-table entries of positions
  * that a call does not reach are not looked at.
  * The arrays are read on the device.  A length that the page table cannot hold
  * is cut, a page outside 0 .. num_pages - 1 is skipped (its keys count as
