@@ -92,6 +92,8 @@ int bitnet_w8a8_forward(const void* x, int x_dtype, const float* norm_w, const i
   DeviceContext* ctx;
   if ((rc = device_context(&ctx))) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (w8a8_forward_few_supported(M, K))
+    return cuda_status(launch_w8a8_forward_few(ctx, x, x_dtype, norm_w, eps, w_codes, w_scale, M, K, N, y, y_dtype, s));
   const bool few = w8a8_few_supported(M);
   const size_t code_bytes = (static_cast<size_t>(M * K) * (few ? 1 : 2) + 255) & ~size_t(255);
   uint8_t* ws = nullptr;

@@ -173,6 +173,11 @@ cudaError_t launch_quant_w8(const float* w, int64_t N, int64_t K, int8_t* codes,
 // Few tokens on int8 codes, more on fp16 codes (launch_w8a8_codes turns one into
 // the other).  pdl: launched to overlap the launch before it, which writes the
 // codes and scales but no weights.
+// The whole projection of one or two tokens in one launch; the same bits as the two-launch form.
+bool w8a8_forward_few_supported(int64_t M, int64_t K);
+cudaError_t launch_w8a8_forward_few(const DeviceContext* ctx, const void* x, int x_dtype, const float* g, float eps,
+                                    const int8_t* w, const float* w_scale, int64_t M, int64_t K, int64_t N, void* y,
+                                    int y_dtype, cudaStream_t s);
 bool w8a8_few_supported(int64_t M);
 cudaError_t launch_w8a8_few(const DeviceContext* ctx, const int8_t* a, const float* a_scale, const int8_t* w,
                             const float* w_scale, int64_t M, int64_t K, int64_t N, void* y, int y_dtype,

@@ -9,6 +9,8 @@
 // products an instruction and token) against the codes, which stay in L1.  The
 // first loads of a warp are issued before the wait for the launch that writes
 // the codes.  From 9 tokens on the tensor cores (w8a8_tc.cu) take over.
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "rowquant.cuh"
@@ -17,6 +19,15 @@ namespace bitnet {
 namespace {
 
 constexpr int kWarps = 8;
+
+// The one-launch form's most tokens, and longest row (its codes stay in 32 KB of
+// shared memory, its fixed-point sums in their range).  Against two launches, per
+// call in a graph with weights out of L2, K x N: one token 4096 x 4096 6.8 against
+// 7.7 us, 4096 x 14336 13.0 / 15.8, 4096 x 131072 79 (6.8 TB/s) / 84; two tokens
+// 9.0 / 9.7, 15.4 / 17.6, 83 / 92, but 14336 x 4096 20.8 / 20.0; single calls 3 us
+// less each (no second launch, no workspace).  Every CTA normalises all rows, so
+// more of them stop paying.
+constexpr int64_t kFusedRows = 2, kFusedK = 16384;
 
 // One warp per output channel: absmax over its K weights, then the codes.
 __global__ void __launch_bounds__(kWarps * 32) k_quant_w8(const float* __restrict__ w, int64_t N, int K,
@@ -128,6 +139,153 @@ __global__ void __launch_bounds__(kWarps * 32) k_w8a8_few(const int8_t* __restri
     }
 }
 
+// The largest of a value's bit patterns over the CTA, for kM rows at once.
+template <int kM>
+__device__ __forceinline__ void cta_max(unsigned (&v)[kM], unsigned (*box)[kWarps], int warp, int lane) {
+#pragma unroll
+  for (int m = 0; m < kM; ++m) {
+    v[m] = __reduce_max_sync(0xffffffffu, v[m]);
+    if (lane == 0) box[m][warp] = v[m];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < kM; ++m)
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) v[m] = max(v[m], box[m][i]);
+}
+
+// The whole projection of kM tokens in one launch: every CTA normalises and
+// quantises the rows itself (sums and maxima that do not depend on their order:
+// the codes of the separate kernel, bit for bit), into shared memory, while the
+// first of its weights are on their way; then, CTAs walking over the weight rows,
+// k_w8a8_few's contraction.
+template <typename InT, int kM, int kR>
+__global__ void __launch_bounds__(kWarps * 32, 2)
+    k_w8a8_forward_few(const InT* __restrict__ x, const float* __restrict__ g, float eps, const int8_t* __restrict__ w,
+                       const float* __restrict__ w_scale, int N, int K, void* __restrict__ y, int y_dtype) {
+  constexpr int kAhead = 8, kT = kWarps * 32;
+  extern __shared__ uint4 s_codes[];  // [kM][K / 16]
+  __shared__ unsigned s_key[kM][kWarps], s_max[kM][kWarps];
+  __shared__ unsigned long long s_sum[kM][kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int chunks = (K + 511) / 512, groups = K >> 2;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const uint4* wr[kR];
+  uint4 wv[kAhead][kR];
+  auto rows = [&](int n0) {
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+      wr[r] = reinterpret_cast<const uint4*>(w + static_cast<int64_t>(min(n0 + r, N - 1)) * K) + lane;
+  };
+  auto fetch = [&](int c0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const bool in = (c0 + i) * 512 + lane * 16 < K;
+#pragma unroll
+      for (int r = 0; r < kR; ++r) wv[i][r] = in ? ld_stream(wr[r] + (c0 + i) * 32) : zero;
+    }
+  };
+  int n0 = (blockIdx.x * kWarps + warp) * kR;
+  rows(n0);
+  fetch(0);
+
+  float as[kM];
+  {
+    unsigned key[kM], amax[kM];
+#pragma unroll
+    for (int m = 0; m < kM; ++m) key[m] = amax[m] = 0u;
+    for (int i = tid; i < groups; i += kT)
+#pragma unroll
+      for (int m = 0; m < kM; ++m)
+        key[m] = max(key[m], static_cast<unsigned>(sq_key4(load4(x + static_cast<int64_t>(m) * K + 4 * i))));
+    cta_max<kM>(key, s_key, warp, lane);
+    float rstd[kM];
+#pragma unroll
+    for (int m = 0; m < kM; ++m) {
+      const float scale = sq_scale(static_cast<int>(key[m]));
+      SqPartial part = {0ull, 0u};
+      int n = 0;  // K <= 16384: at most 64 values
+      for (int i = tid; i < groups; i += kT, n += 4) sq_add4(part, load4(x + static_cast<int64_t>(m) * K + 4 * i), scale);
+      const unsigned long long sum = warp_sum_u64(sq_fold(part, n));
+      if (lane == 0) s_sum[m][warp] = sum;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < kM; ++m) {
+      unsigned long long sum = 0ull;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) sum += s_sum[m][i];
+      rstd[m] = rstd_from_fixed(sum, static_cast<int>(key[m]), K, eps);
+    }
+    auto normed = [&](int m, int i, float4 gv) {
+      const float4 v = load4(x + static_cast<int64_t>(m) * K + 4 * i);
+      return make_float4(norm_elem(v.x, rstd[m], gv.x), norm_elem(v.y, rstd[m], gv.y), norm_elem(v.z, rstd[m], gv.z),
+                         norm_elem(v.w, rstd[m], gv.w));
+    };
+    for (int i = tid; i < groups; i += kT) {
+      const float4 gv = __ldg(reinterpret_cast<const float4*>(g) + i);
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        const float4 v = normed(m, i, gv);
+        amax[m] = max(amax[m], __float_as_uint(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)))));
+      }
+    }
+    cta_max<kM>(amax, s_max, warp, lane);
+#pragma unroll
+    for (int m = 0; m < kM; ++m) as[m] = act_scale_from_amax(__uint_as_float(amax[m]));
+    uint32_t* codes = reinterpret_cast<uint32_t*>(s_codes);
+    for (int i = tid; i < groups; i += kT) {
+      const float4 gv = __ldg(reinterpret_cast<const float4*>(g) + i);
+#pragma unroll
+      for (int m = 0; m < kM; ++m) codes[m * groups + i] = quant_pack4_i8(normed(m, i, gv), as[m]);
+    }
+    __syncthreads();
+  }
+
+  const int step = static_cast<int>(gridDim.x) * kWarps * kR;
+  while (n0 < N) {
+    int acc[kM][kR];
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int r = 0; r < kR; ++r) acc[m][r] = 0;
+    for (int c0 = 0; c0 < chunks; c0 += kAhead) {
+      if (c0) fetch(c0);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int k = (c0 + i) * 512 + lane * 16;
+        if (k >= K) break;
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+          const uint4 v = s_codes[(m * K + k) >> 4];
+#pragma unroll
+          for (int r = 0; r < kR; ++r) {
+            acc[m][r] = __dp4a(static_cast<int>(wv[i][r].x), static_cast<int>(v.x), acc[m][r]);
+            acc[m][r] = __dp4a(static_cast<int>(wv[i][r].y), static_cast<int>(v.y), acc[m][r]);
+            acc[m][r] = __dp4a(static_cast<int>(wv[i][r].z), static_cast<int>(v.z), acc[m][r]);
+            acc[m][r] = __dp4a(static_cast<int>(wv[i][r].w), static_cast<int>(v.w), acc[m][r]);
+          }
+        }
+      }
+    }
+    const int at0 = n0;
+    n0 += step;
+    if (n0 < N) {
+      rows(n0);
+      fetch(0);
+    }
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        const int sum = warp_sum_int(acc[m][r]);
+        if (lane == m * kR + r && at0 + r < N)
+          store_y(y, y_dtype, static_cast<int64_t>(m) * N + at0 + r,
+                  rescale_elem(static_cast<float>(sum), __frcp_rn(as[m]), __frcp_rn(__ldg(w_scale + at0 + r))));
+      }
+  }
+}
+
 // int8 codes as fp16 (exact), 16 a thread.
 __global__ void __launch_bounds__(256) k_w8a8_codes(const int8_t* __restrict__ in, __half* __restrict__ out,
                                                     int64_t n16) {
@@ -164,12 +322,47 @@ cudaError_t launch_few(const DeviceContext* ctx, const int8_t* a, const float* a
   return cudaLaunchKernelEx(&cfg, kern, a, a_scale, w, w_scale, M, N, K, y, y_dtype, acc_out);
 }
 
+template <typename InT, int kM>
+cudaError_t launch_forward_few(const DeviceContext* ctx, const void* x, const float* g, float eps, const int8_t* w,
+                               const float* w_scale, int N, int K, void* y, int y_dtype, cudaStream_t s) {
+  const int64_t warps = static_cast<int64_t>(ctx->num_sms) * kWarps;
+  const int kr = N >= 2 * warps ? 2 : 1;  // as launch_few's
+  const int64_t ctas = (static_cast<int64_t>(N) + kr * kWarps - 1) / (kr * kWarps);
+  const unsigned grid = static_cast<unsigned>(ctas < 2 * ctx->num_sms ? ctas : 2 * ctx->num_sms);
+  const InT* xt = static_cast<const InT*>(x);
+  const size_t smem = static_cast<size_t>(kM) * K;
+  if (kr == 2)
+    k_w8a8_forward_few<InT, kM, 2><<<grid, kWarps * 32, smem, s>>>(xt, g, eps, w, w_scale, N, K, y, y_dtype);
+  else
+    k_w8a8_forward_few<InT, kM, 1><<<grid, kWarps * 32, smem, s>>>(xt, g, eps, w, w_scale, N, K, y, y_dtype);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_quant_w8(const float* w, int64_t N, int64_t K, int8_t* codes, float* scale, cudaStream_t s) {
   k_quant_w8<<<static_cast<unsigned>((N + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(w, N, static_cast<int>(K), codes,
                                                                                      scale);
   return cudaGetLastError();
+}
+
+bool w8a8_forward_few_supported(int64_t M, int64_t K) { return M <= kFusedRows && K <= kFusedK; }
+
+cudaError_t launch_w8a8_forward_few(const DeviceContext* ctx, const void* x, int x_dtype, const float* g, float eps,
+                                    const int8_t* w, const float* w_scale, int64_t M, int64_t K, int64_t N, void* y,
+                                    int y_dtype, cudaStream_t s) {
+  const int n = static_cast<int>(N), k = static_cast<int>(K);
+  auto go = [&](auto* t) {
+    using InT = std::remove_pointer_t<decltype(t)>;
+    return M == 1 ? launch_forward_few<InT, 1>(ctx, x, g, eps, w, w_scale, n, k, y, y_dtype, s)
+                  : launch_forward_few<InT, 2>(ctx, x, g, eps, w, w_scale, n, k, y, y_dtype, s);
+  };
+  switch (x_dtype) {
+    case BITNET_DTYPE_F32: return go(static_cast<float*>(nullptr));
+    case BITNET_DTYPE_F16: return go(static_cast<__half*>(nullptr));
+    case BITNET_DTYPE_BF16: return go(static_cast<__nv_bfloat16*>(nullptr));
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 bool w8a8_few_supported(int64_t M) { return M <= 8; }

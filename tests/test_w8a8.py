@@ -161,6 +161,22 @@ def test_forward_is_its_steps(device, M, K, N, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("M", [1, 2, 3])
+@pytest.mark.parametrize("K,N", [(128, 1), (2176, 33), (16384, 20), (16512, 20), (256, 20011)])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_forward_of_few_tokens(device, M, K, N, dtype):
+    """The one-launch form's ends: row lengths up to its limit and past it, more output rows than its CTAs hold at a
+    time, tokens of very different size; every bit that of the entry points one by one."""
+    r = np.random.default_rng(6)
+    x = torch.from_numpy(r.standard_normal((M, K)).astype(np.float32)).to(dtype).cuda()
+    x *= torch.tensor([1e-4, 0.0, 100.0], device="cuda", dtype=dtype)[:M, None]
+    g = torch.from_numpy((1 + 0.1 * r.standard_normal(K)).astype(np.float32)).cuda()
+    w, sw = bn.quant_w8(torch.from_numpy((0.02 * r.standard_normal((N, K))).astype(np.float32)).cuda())
+    a, sa, _ = bn.rmsnorm_quant_a8(x.float(), g)
+    assert torch.equal(bn.w8a8_forward(x, g, w, sw, y_dtype=F32), bn.w8a8_gemm(a, sa, w, sw, y_dtype=F32))
+
+
+@gpu
 @pytest.mark.parametrize("M", [1, 20, 200])
 def test_streams_and_graphs(device, M):
     K, N = 2048, 520
