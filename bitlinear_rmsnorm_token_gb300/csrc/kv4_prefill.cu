@@ -12,17 +12,31 @@
 // with C the cache's codes as c - 8 in fp16, exact; the scales stay out of the
 // products (kv4.cuh).  O, S and W live in tensor memory; W takes S's place.
 // A row's reference only moves when its maximum has grown by 2^8 (O is then
-// rescaled), so most pages are taken without a maximum, scores to W in one pass; W is kept in fp16's range by a power of two of the largest value
-// scale met, which moves in the same way.  fp32 queries and their W are two fp16
-// parts each (22 bits), two products where 16-bit ones take one.
+// rescaled), so most pages are taken without a maximum, scores to W in one pass.
+// W is kept in fp16's range by a power of two of the largest value scale met,
+// which moves in the same way.  fp32 queries and their W are two fp16 parts each
+// (22 bits), two products where 16-bit ones take one.
 //
-// Warps: 4 per tile for the softmax (a thread a row), 4 that decode pages into
-// the operands' swizzled layout (values transposed: rows are dimensions, in the
-// order that keeps the stores of a warp on different banks), a producer of raw
-// pages, and an MMA issuer per tile.  S is double buffered, so that the next
+// Warps: 4 per tile for the softmax (a thread a row), 4 (8 for heads of 256) that
+// decode pages into the operands' swizzled layout (values transposed: rows are
+// dimensions, in the order that keeps the stores of a warp on different banks), a
+// producer of raw pages, and an MMA issuer per tile.  Softmax and decode warps
+// first share the work of the queries.  S is double buffered, so that the next
 // page's scores are computed while a page's softmax runs.
 // Few tiles on a long cache: the pages are split over gridDim.z and the parts
 // joined by a second launch, in order.
+//
+// Measured: 4096 tokens behind 8192 others, 16 query heads of 128 on 8, causal,
+// bf16: 415 us, 0.83 PFLOP/s.  The tensor cores are busy for two fifths of it: the
+// softmax and the decoding set the pace (0.57 instructions a cycle and scheduler,
+// with 3 to 4 warps each), about 2400 cycles a page and CTA, and 256 CTAs on 152
+// SMs leave a tenth idle at the end.  64 texts of up to 512 tokens, 4 heads of 256
+// on one, both directions: 80 us, half of it the CTAs' beginnings and ends (88
+// with the queries left to the softmax warps).
+// Tried and slower: CTAs that walk over equal shares of all pages (450 and 110
+// us: no idle end, but the page loop's code comes out slower and pieces cost
+// more), results through shared memory (423 and 93), bf16 operands met as fp16
+// (449), three stages of keys and values (437), waits that sleep (428 and more).
 #include <type_traits>
 
 #include "common.cuh"
@@ -102,6 +116,45 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, 
       : "memory");
 }
 
+// Largest magnitude of 8 values.
+template <typename QT>
+__device__ __forceinline__ float top8(const uint4* raw) {
+  if constexpr (sizeof(QT) == 4) {
+    const float* x = reinterpret_cast<const float*>(raw);
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+    return top;
+  } else {  // 16-bit magnitudes are ordered as their bits
+    const uint32_t m = 0x7fff7fffu;
+    const uint32_t t = __vmaxu2(__vmaxu2(raw->x & m, raw->y & m), __vmaxu2(raw->z & m, raw->w & m));
+    const uint16_t b = static_cast<uint16_t>(max(t & 0xffffu, t >> 16));
+    return static_cast<float>(*reinterpret_cast<const QT*>(&b));
+  }
+}
+
+// v[k] of the kLanes lanes of a row group reduced together for 8 rows k: lane i
+// gets row i % 8 (a lane sends half of what it holds at each of three steps).
+template <int kLanes, typename F>
+__device__ __forceinline__ float rows_reduce(const float (&v)[8], int lane, F op) {
+  float a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float send = lane & 1 ? v[2 * i] : v[2 * i + 1], keep = lane & 1 ? v[2 * i + 1] : v[2 * i];
+    a[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 1));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float send = lane & 2 ? a[2 * i] : a[2 * i + 1], keep = lane & 2 ? a[2 * i + 1] : a[2 * i];
+    b[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 2));
+  }
+  const float send = lane & 4 ? b[0] : b[1], keep = lane & 4 ? b[1] : b[0];
+  float r = op(keep, __shfl_xor_sync(0xffffffffu, send, 4));
+#pragma unroll
+  for (int o = 8; o < kLanes; o <<= 1) r = op(r, __shfl_xor_sync(0xffffffffu, r, o));
+  return r;
+}
+
 // A page's per-key factors, and what the softmax has to know of the page.
 struct __align__(16) PageMeta {
   float ks[kKvPage], kmid[kKvPage];  // s, m + 8 s of the keys
@@ -121,15 +174,21 @@ struct Layout {
   static constexpr int kV = D == 256 && kSplit ? 1 : 2;      // value operand stages
   static constexpr int kUnpackWarps = D == 256 ? 8 : 4;
   static constexpr int kMeta = 4;
+  static constexpr int kQSteps = D == 128 ? 4 : 8;  // rows of a lane at a time while 12 warps share the queries
   static constexpr int kSoftWarps = 4 * kT;
   static constexpr int kProducer = kSoftWarps + kUnpackWarps;  // then an MMA warp per tile
   static constexpr int kMma0 = kProducer + 1;
   static constexpr int kThreads = 512;
+  // registers a thread, of 128 at the launch: warps 0 .. 3, 4 .. 7, 8 .. 11 and 12 .. 15 share a role's number
+  static constexpr int kSoftRegs = D == 128 ? 168 : 200, kUnpackRegs = D == 128 ? 88 : 104, kOtherRegs = kUnpackRegs;
+  static_assert(kT * kSoftRegs + kUnpackWarps / 4 * kUnpackRegs + kOtherRegs <= 4 * 128, "more registers than the launch has");
+  static_assert(kSoftWarps % 4 == 0 && kUnpackWarps % 4 == 0 && kProducer == 12, "roles by four warps");
   static_assert(kMma0 + kT <= kThreads / 32, "roles");
   static constexpr int kQPart = kRows * D * 2;               // bytes of one part of a tile's queries
   static constexpr int kOp = kKvPage * D * 2;                // bytes of a page's keys (values) as fp16
   static constexpr int offQ = 0;
-  static constexpr int offK = offQ + kT * kParts * kQPart;
+  static constexpr int kQTile = kParts * kQPart;             // of a tile's queries
+  static constexpr int offK = offQ + kT * kQTile;
   static constexpr int offV = offK + kK * kOp;
   static constexpr int offRaw = offV + kV * kOp;
   static constexpr int offMeta = offRaw + kRaw * KvBlock<D>::kBytes;
@@ -149,12 +208,24 @@ struct Layout {
 struct Problem {
   KvView c;
   int Hq, G, T, max_q;
+  uint32_t g_mul;  // row / G = row g_mul >> g_shift for rows below 2^31
+  int g_shift;
   float scale;  // |softmax scale| * log2(e)
   float sign;   // its sign, given to the queries
   int causal, window;
   unsigned* err;
   float* part;  // [splits][T * Hq][D + 4], or null
 };
+
+// The token of row `row` of an item, and where the row's head lies in q and out.
+__device__ __forceinline__ int token_of(const Problem& p, int row) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(row)) * p.g_mul) >> p.g_shift);
+}
+template <int D>
+__device__ __forceinline__ int64_t row_at(const Problem& p, int q0, int head, int row) {
+  const int i = token_of(p, row);
+  return (static_cast<int64_t>(q0 + i) * p.Hq + head * p.G + (row - i * p.G)) * D;
+}
 
 template <int D, bool kSplit, typename QT, typename OT>
 __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
@@ -215,7 +286,7 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
       mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&drained[i], 1);
-      mbar_init(&q_full[i], 4);
+      mbar_init(&q_full[i], 1);
       mbar_init(&o_done[i], 1);
     }
     *abort_flag = 0;
@@ -294,79 +365,76 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // ---- queries, scaled by a power of two per row, as fp16 (one part or two), by the softmax and the unpack warps, up to
+  // 8 rows of a lane at a time: D / 8 lanes to a row, 8 dimensions each
+  float2* row_q = reinterpret_cast<float2*>(smem + L::offRow);
+  if (warp < L::kProducer) {
+    constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes of a row, rows of a warp at a time
+    constexpr int kStep = L::kQSteps, kBlocks = kT * kRows / (kStep * kAt);
+    const int c = lane % kLanes, sub = lane / kLanes;
+    auto place = [&](int rt) {  // of chunk c of a row (8 dimensions), in each part of the operand
+      const int tile = rt / kRows, r = rt % kRows;
+      return smem + L::offQ + tile * L::kQTile + (c >> 3) * (kRows * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
+             (((c & 7) ^ (r & 7)) << 4);
+    };
+    for (int blk = warp; blk < kBlocks; blk += L::kProducer) {
+      const int rt0 = blk * kStep * kAt + sub;
+      uint4 raw[8][L::kParts];
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) {
+        const int row = row0 + rt0 + k * kAt;
+        const uint4* src = reinterpret_cast<const uint4*>(q + (row < rows ? row_at<D>(p, q0, head, row) + 8 * c : 0));
+#pragma unroll
+        for (int u = 0; u < L::kParts; ++u) raw[k][u] = row < rows ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = k < kStep ? top8<QT>(raw[k]) : 0.0f;
+      const int e = pow2_exp(rows_reduce<kLanes>(v, lane, [](float x, float y) { return fmaxf(x, y); }));
+      const float f_row = p.sign * pow2(14 - e);  // of row lane % 8 of the eight
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) {
+        const float f = __shfl_sync(0xffffffffu, f_row, (lane & ~7) | k);
+        const QT* x = reinterpret_cast<const QT*>(raw[k]);
+        // chunk c of the row: dimensions 8c + 0, 4, 1, 5, 2, 6, 3, 7, the order in which a word of codes decodes
+        uint8_t* dst = place(rt0 + k * kAt);
+        float y[8], sum = 0.0f;
+        uint32_t h[4];
+#pragma unroll
+        for (int d = 0; d < 8; ++d) y[d] = static_cast<float>(x[d]) * f;
+#pragma unroll
+        for (int part = 0; part < L::kParts; ++part) {
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            h[d] = pack_h2(y[d], y[d + 4]);
+            const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&h[d]));
+            sum += z.x + z.y;
+            y[d] -= z.x;
+            y[d + 4] -= z.y;
+          }
+          *reinterpret_cast<uint4*>(dst + part * L::kQPart) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        v[k] = sum;
+      }
+      const float sum = rows_reduce<kLanes>(v, lane, [](float x, float y) { return x + y; });
+      if (c < kStep) row_q[rt0 + c * kAt] = make_float2(sum, p.scale * pow2(e - 14));
+    }
+    fence_proxy_async_smem();
+    // they meet: a thread reads its row's factors, which another warp may have written
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * L::kProducer) : "memory");
+    if (threadIdx.x == 0)
+      for (int t = 0; t < kT; ++t) mbar_arrive(&q_full[t]);
+  }
+
   if (warp < L::kSoftWarps) {
     // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftRegs));
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;  // this warp's quarter of the TMEM lanes
     const int tile = warp >> 2;
-    // ---- queries, scaled by a power of two per row, as fp16 (one part or two): D / 8 lanes to a row, 8 dimensions
-    // each, the loads of 8 rows in flight
-    float2* row_q = reinterpret_cast<float2*>(smem + L::offRow);
-    {
-      constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes of a row, rows of a warp at a time
-      constexpr int kStep = 4 * kAt, kBatch = 8;
-      constexpr int kVecs = sizeof(QT) / 2;             // 16-byte loads of 8 dimensions
-      const int c = lane % kLanes;
-#pragma unroll 1
-      for (int t0 = (warp & 3) * kAt + lane / kLanes; t0 < kRows; t0 += kBatch * kStep) {
-        uint4 raw[kBatch][kVecs];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int row = row0 + tile * kRows + t0 + k * kStep;
-          const int i = row / p.G;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              q + (static_cast<int64_t>(q0 + i) * p.Hq + head * p.G + (row - i * p.G)) * D + 8 * c);
-#pragma unroll
-          for (int u = 0; u < kVecs; ++u) raw[k][u] = row < rows ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int rt = t0 + k * kStep;
-          const QT* x = reinterpret_cast<const QT*>(raw[k]);
-          float v[8], top = 0.0f;
-#pragma unroll
-          for (int d = 0; d < 8; ++d) {
-            v[d] = static_cast<float>(x[d]);
-            top = fmaxf(top, fabsf(v[d]));
-          }
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const int e = pow2_exp(top);
-          const float f = p.sign * pow2(14 - e);
-          // chunk c of the row: dimensions 8c + 0, 4, 1, 5, 2, 6, 3, 7, the order in which a word of codes decodes
-          uint8_t* dst = smem + L::offQ + tile * L::kParts * L::kQPart + (c >> 3) * (kRows * 128) + (rt >> 3) * 1024 +
-                         (rt & 7) * 128 + (((c & 7) ^ (rt & 7)) << 4);
-          float h[8], sum = 0.0f;
-#pragma unroll
-          for (int d = 0; d < 8; ++d) {
-            v[d] *= f;
-            h[d] = __half2float(__float2half_rn(v[d]));
-            sum += h[d];
-          }
-          *reinterpret_cast<uint4*>(dst) =
-              make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
-          if constexpr (kSplit) {
-#pragma unroll
-            for (int d = 0; d < 8; ++d) {
-              h[d] = __half2float(__float2half_rn(v[d] - h[d]));
-              sum += h[d];
-            }
-            *reinterpret_cast<uint4*>(dst + L::kQPart) =
-                make_uint4(pack_h2(h[0], h[4]), pack_h2(h[1], h[5]), pack_h2(h[2], h[6]), pack_h2(h[3], h[7]));
-          }
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (c == 0) row_q[tile * kRows + rt] = make_float2(sum, p.scale * pow2(e - 14));
-        }
-      }
-      fence_proxy_async_smem();
-    }
-    // the tile's four warps meet: a thread reads its row's factors, which another warp may have written
-    asm volatile("bar.sync %0, 128;" ::"r"(tile + 1) : "memory");
-    if (lane == 0) mbar_arrive(&q_full[tile]);
     const int tile_r0 = row0 + tile * kRows;
     const int r = tile_r0 + (threadIdx.x & 127);  // row of the item
     const bool row_on = r < rows;
-    const int i_tok = row_on ? r / p.G : 0;
+    const int i_tok = row_on ? token_of(p, r) : 0;
     const int64_t q_at = static_cast<int64_t>(q0 + i_tok) * p.Hq + head * p.G + (row_on ? r - i_tok * p.G : 0);
     const float2 row = row_q[threadIdx.x];
     const float qc = row.y;
@@ -622,6 +690,7 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
     }
   } else if (warp < L::kProducer) {
     // ------------------------------------------------------------ unpack
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kUnpackRegs));
     constexpr int kU = 32 * L::kUnpackWarps;
     const int ut = threadIdx.x - 32 * L::kSoftWarps;  // 0 .. kU - 1
     constexpr int kWords = D / 8;                     // words of a row
@@ -724,6 +793,7 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
       }
     }
   } else if (warp == L::kProducer) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kOtherRegs));
     // ------------------------------------------------------------ raw pages
     if (lane == 0) {
       int j = 0;
@@ -744,11 +814,12 @@ __global__ void __launch_bounds__(Layout<D, kSplit>::kThreads, 1)
         for (int i = max(0, j - L::kRaw); i < j; ++i) mbar_wait(&raw_full[i % L::kRaw], (i / L::kRaw) & 1, p.err);
     }
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kOtherRegs));
     // ------------------------------------------------------------ MMA issue, a warp per tile
     if (warp < L::kMma0 + kT && lane == 0) {
       const int t = warp - L::kMma0;
       constexpr uint32_t id_s = idesc_f16_f32(kRows, kKvPage), id_o = idesc_f16_f32(kRows, D);
-      const uint32_t q_addr = smem_u32(smem + L::offQ + t * L::kParts * L::kQPart);
+      const uint32_t q_addr = smem_u32(smem + L::offQ + t * L::kQTile);
       auto scores = [&](int j) {
         const int ks = j % L::kK;
         if (!mbar_wait(&k_full[ks], (j / L::kK) & 1, p.err, abort_flag)) return false;
@@ -910,6 +981,10 @@ cudaError_t launch_kv4_prefill(DeviceContext* ctx, const KvView& c, int head_dim
   p.T = static_cast<int>(T);
   p.max_q = max_q_len;
   p.scale = fabsf(scale) * 1.4426950408889634f;
+  int l = 0;
+  while ((1 << l) < p.G) ++l;
+  p.g_mul = static_cast<uint32_t>(((int64_t{1} << (31 + l)) + p.G - 1) / p.G);
+  p.g_shift = 31 + l;
   p.sign = scale < 0.0f ? -1.0f : 1.0f;
   p.causal = causal;
   p.window = window < (1 << 30) ? window : 1 << 30;  // keeps position - window within 32 bits
