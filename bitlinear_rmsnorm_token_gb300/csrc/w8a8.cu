@@ -4,11 +4,14 @@
 // acc[m, n] = sum_k a[m, k] w[n, k] in int32, y = ((float)acc * (1 / a_scale[m]))
 // * (1 / w_scale[n]) with every operation rounded on its own.
 //
-// Up to 8 tokens the weights' N K bytes are all that counts: a warp streams kR
-// rows of them with 16-byte loads, many in flight, and multiplies with dp4a (4
-// products an instruction and token) against the codes, which stay in L1.  The
-// first loads of a warp are issued before the wait for the launch that writes
-// the codes.  From 9 tokens on the tensor cores (w8a8_tc.cu) take over.
+// Up to 16 tokens the weights' N K bytes are all that counts.  One or two tokens: a
+// warp streams kR rows of them with 16-byte loads, many in flight, and multiplies
+// with dp4a (4 products an instruction and token) against the codes, which stay in
+// L1.  3 to 16: the weights still go straight to registers, but into mma.sync with
+// the tokens as its 8 columns.  The first loads of a warp are issued before the wait
+// for the launch that writes the codes.  From 17 tokens on tcgen05 (w8a8_tc.cu).
+// One token, 4096 x 4096: 5.5 us with the weights out of L2; 8192 x 8192: 13.7 us
+// (4.9 TB/s).
 #include <type_traits>
 
 #include "common.cuh"
@@ -19,6 +22,9 @@ namespace bitnet {
 namespace {
 
 constexpr int kWarps = 8;
+// Tokens up to which dp4a and mma.sync take the product.  Two tokens, dp4a against
+// mma.sync: 2048 x 2048 3.1 / 3.7 us, 4096 x 4096 6.3 / 6.4, 8192 x 8192 16.5 / 15.0.
+constexpr int64_t kFew = 2, kSome = 16;
 
 // The one-launch form's most tokens, and longest row (its codes stay in 32 KB of
 // shared memory, its fixed-point sums in their range).  Against two launches, per
@@ -66,22 +72,22 @@ __device__ __forceinline__ void store_y(void* y, int y_dtype, int64_t at, float 
 
 __device__ __forceinline__ uint4 ld_stream(const uint4* p) {  // read once: not kept in L1
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
 }
 
-// A warp takes kR consecutive rows; kM tokens (rows past M repeat the last and
-// are not stored).  Chunk i of a row is its bytes 512 i + 16 lane ...
+// A warp takes kR consecutive rows; kM tokens.  Chunk i of a row is its bytes
+// 512 i + 16 lane ...
 template <int kM, int kR>
 __global__ void __launch_bounds__(kWarps * 32) k_w8a8_few(const int8_t* __restrict__ a,
                                                           const float* __restrict__ a_scale,
                                                           const int8_t* __restrict__ w,
-                                                          const float* __restrict__ w_scale, int M, int N, int K,
+                                                          const float* __restrict__ w_scale, int N, int K,
                                                           void* __restrict__ y, int y_dtype,
                                                           int32_t* __restrict__ acc_out) {
-  constexpr int kAhead = kR == 4 ? 4 : 8;  // chunks of every row in flight
+  constexpr int kAhead = 8;  // chunks of every row in flight
   const int lane = threadIdx.x & 31;
   const int n0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kR;
   const int chunks = (K + 511) / 512;
@@ -114,7 +120,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_w8a8_few(const int8_t* __restri
       if (k >= K) break;
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
-        const uint4 v = *reinterpret_cast<const uint4*>(a + static_cast<int64_t>(min(m, M - 1)) * K + k);
+        const uint4 v = *reinterpret_cast<const uint4*>(a + static_cast<int64_t>(m) * K + k);
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
           acc[m][r] = __dp4a(static_cast<int>(wv[i][r].x), static_cast<int>(v.x), acc[m][r]);
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_w8a8_few(const int8_t* __restri
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       const int sum = warp_sum_int(acc[m][r]);
-      if (lane == (m * kR + r) % 32 && m < M && n0 + r < N) {
+      if (lane == m * kR + r && n0 + r < N) {
         const int64_t at = static_cast<int64_t>(m) * N + n0 + r;
         store_y(y, y_dtype, at,
                 rescale_elem(static_cast<float>(sum), __frcp_rn(a_scale[m]), __frcp_rn(__ldg(w_scale + n0 + r))));
@@ -286,6 +292,142 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   }
 }
 
+// D += A B, one m16n8k16 fp16 product (rows x k: A, k x columns: B).
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Some tokens: a CTA takes 16 kTiles channels and 8 kNB tokens; its kW warps share
+// K, four chunks of 64 at a time (256 consecutive bytes of a row).  Weights go from
+// memory to registers, kAhead chunks in flight, and as fp16 (exact) into
+// mma.m16n8k16 as the 16-row side: a lane's 16 bytes of a row are its share of four
+// products, K in an order of its own that the tokens' bytes follow.  The fp32 sums
+// take kFold chunks (at most 512 of K: at most 2^23, exact) and then join the warp's
+// int32 sums in shared memory, where the warps' meet in the end.
+// 13 tokens, 8192 x 8192: 19 us with the weights out of L2 (3.5 TB/s), 4096 x 4096:
+// 7.4 us, against 21 and 11.8 us of the tcgen05 kernel, whose 128-channel tiles,
+// TMEM operand and cluster exchange pay from more tokens on (24 tokens: 22 us
+// against 39); 8 tokens 15 and 6.4 us, where dp4a took 37 and 10.4.  Chunks dealt to
+// the warps one by one (64 bytes of a row at a time) cost 22 us, 16 channels a
+// CTA 21 us, four chunks ahead (spills) 21 us.
+template <int kNB, int kTiles, int kW>
+__global__ void __launch_bounds__(kW * 32, 16 / kW)
+    k_w8a8_some(const int8_t* __restrict__ a, const float* __restrict__ a_scale, const int8_t* __restrict__ w,
+                const float* __restrict__ w_scale, int M, int N, int K, void* __restrict__ y, int y_dtype,
+                int32_t* __restrict__ acc_out) {
+  constexpr int kAhead = kTiles == 1 ? 8 : 3, kFold = kTiles == 1 ? 8 : 6, kRows = 16 * kTiles, kCols = 8 * kNB;
+  __shared__ int s_part[kW][kCols][kRows + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * kRows;
+  const int chunks = K / 64;
+  const int mine = chunks / (4 * kW) * 4 + min(max(chunks % (4 * kW) - 4 * warp, 0), 4);  // of this warp
+  auto at = [](int c) { return (c >> 2) * (16 * kW) + 4 * (c & 3); };  // this warp's chunk c, in 16 bytes
+  const uint4* wr[2 * kTiles];
+#pragma unroll
+  for (int r = 0; r < 2 * kTiles; ++r)
+    wr[r] = reinterpret_cast<const uint4*>(w + static_cast<int64_t>(min(n0 + 8 * r + g, N - 1)) * K) + 16 * warp + t;
+  const uint4* ar[kNB];
+#pragma unroll
+  for (int b = 0; b < kNB; ++b)
+    ar[b] = reinterpret_cast<const uint4*>(a + static_cast<int64_t>(min(8 * b + g, M - 1)) * K) + 16 * warp + t;
+  uint4 wv[kAhead][2 * kTiles], av[kNB];
+  auto fetch = [&](int i, int c) {
+#pragma unroll
+    for (int r = 0; r < 2 * kTiles; ++r) wv[i][r] = ld_stream(wr[r] + at(c));
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (i < mine) fetch(i, i);
+  pdl_wait();  // the codes come from the launch before this one
+  if (mine > 0) {
+#pragma unroll
+    for (int b = 0; b < kNB; ++b) av[b] = *ar[b];
+  }
+  float acc[kTiles][kNB][4];
+  auto fold = [&](bool first) {
+#pragma unroll
+    for (int r = 0; r < kTiles; ++r)
+#pragma unroll
+      for (int b = 0; b < kNB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          int& sum = s_part[warp][8 * b + 2 * t + (j & 1)][16 * r + g + 8 * (j >> 1)];
+          sum = first ? 0 : sum + static_cast<int>(acc[r][b][j]);
+          acc[r][b][j] = 0.0f;
+        }
+  };
+  fold(true);
+  for (int c0 = 0; c0 < mine; c0 += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int c = c0 + i;
+      if (c >= mine) break;
+      uint32_t bl[kNB][4], bh[kNB][4];
+#pragma unroll
+      for (int b = 0; b < kNB; ++b) {
+        int8_to_h2(av[b].x, bl[b][0], bh[b][0]);
+        int8_to_h2(av[b].y, bl[b][1], bh[b][1]);
+        int8_to_h2(av[b].z, bl[b][2], bh[b][2]);
+        int8_to_h2(av[b].w, bl[b][3], bh[b][3]);
+        if (c + 1 < mine) av[b] = ar[b][at(c + 1)];
+      }
+#pragma unroll
+      for (int r = 0; r < kTiles; ++r) {
+        const uint32_t lo[4] = {wv[i][2 * r].x, wv[i][2 * r].y, wv[i][2 * r].z, wv[i][2 * r].w};
+        const uint32_t hi[4] = {wv[i][2 * r + 1].x, wv[i][2 * r + 1].y, wv[i][2 * r + 1].z, wv[i][2 * r + 1].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t a0, a1, a2, a3;
+          int8_to_h2(lo[k], a0, a2);
+          int8_to_h2(hi[k], a1, a3);
+#pragma unroll
+          for (int b = 0; b < kNB; ++b) mma16816(acc[r][b], a0, a1, a2, a3, bl[b][k], bh[b][k]);
+        }
+      }
+      if (c + kAhead < mine) fetch(i, c + kAhead);
+    }
+    if ((c0 + kAhead) % kFold == 0) fold(false);
+  }
+  fold(false);
+  __syncthreads();
+  for (int o = threadIdx.x; o < kRows * kCols; o += kW * 32) {
+    const int m = o / kRows, n = n0 + o % kRows;
+    int v = 0;
+#pragma unroll
+    for (int i = 0; i < kW; ++i) v += s_part[i][m][o % kRows];
+    if (m < M && n < N) {
+      const int64_t to = static_cast<int64_t>(m) * N + n;
+      store_y(y, y_dtype, to, rescale_elem(static_cast<float>(v), __frcp_rn(a_scale[m]), __frcp_rn(__ldg(w_scale + n))));
+      if (acc_out) acc_out[to] = v;
+    }
+  }
+}
+
+template <int kNB>
+cudaError_t launch_some(const DeviceContext* ctx, const int8_t* a, const float* a_scale, const int8_t* w,
+                        const float* w_scale, int M, int N, int K, void* y, int y_dtype, int32_t* acc_out, bool pdl,
+                        cudaStream_t s) {
+  // 32 channels a CTA if that leaves every SM one; 4 warps a CTA if 8 would be more than the SMs hold at a time
+  const bool wide = N >= 32 * ctx->num_sms, many = N > 64 * ctx->num_sms;
+  const int rows = wide ? 32 : 16;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(N) + rows - 1) / rows));
+  cfg.blockDim = dim3(many ? 128 : 256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto kern = many ? k_w8a8_some<kNB, 2, 4> : (wide ? k_w8a8_some<kNB, 2, 8> : k_w8a8_some<kNB, 1, 8>);
+  return cudaLaunchKernelEx(&cfg, kern, a, a_scale, w, w_scale, M, N, K, y, y_dtype, acc_out);
+}
+
 // int8 codes as fp16 (exact), 16 a thread.
 __global__ void __launch_bounds__(256) k_w8a8_codes(const int8_t* __restrict__ in, __half* __restrict__ out,
                                                     int64_t n16) {
@@ -304,11 +446,11 @@ __global__ void __launch_bounds__(256) k_w8a8_codes(const int8_t* __restrict__ i
 
 template <int kM>
 cudaError_t launch_few(const DeviceContext* ctx, const int8_t* a, const float* a_scale, const int8_t* w,
-                       const float* w_scale, int M, int N, int K, void* y, int y_dtype, int32_t* acc_out, bool pdl,
+                       const float* w_scale, int N, int K, void* y, int y_dtype, int32_t* acc_out, bool pdl,
                        cudaStream_t s) {
   // rows per warp: as many as leave every SM eight warps
   const int64_t warps = static_cast<int64_t>(ctx->num_sms) * kWarps;
-  const int kr = N >= 4 * warps && kM > 2 ? 4 : (N >= 2 * warps ? 2 : 1);
+  const int kr = N >= 2 * warps ? 2 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(N) + kr * kWarps - 1) / (kr * kWarps)));
   cfg.blockDim = dim3(kWarps * 32);
@@ -318,8 +460,8 @@ cudaError_t launch_few(const DeviceContext* ctx, const int8_t* a, const float* a
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kern = kr == 4 ? k_w8a8_few<kM, 4> : (kr == 2 ? k_w8a8_few<kM, 2> : k_w8a8_few<kM, 1>);
-  return cudaLaunchKernelEx(&cfg, kern, a, a_scale, w, w_scale, M, N, K, y, y_dtype, acc_out);
+  auto kern = kr == 2 ? k_w8a8_few<kM, 2> : k_w8a8_few<kM, 1>;
+  return cudaLaunchKernelEx(&cfg, kern, a, a_scale, w, w_scale, N, K, y, y_dtype, acc_out);
 }
 
 template <typename InT, int kM>
@@ -365,17 +507,18 @@ cudaError_t launch_w8a8_forward_few(const DeviceContext* ctx, const void* x, int
   }
 }
 
-bool w8a8_few_supported(int64_t M) { return M <= 8; }
+bool w8a8_few_supported(int64_t M) { return M <= kSome; }
 
 cudaError_t launch_w8a8_few(const DeviceContext* ctx, const int8_t* a, const float* a_scale, const int8_t* w,
                             const float* w_scale, int64_t M, int64_t K, int64_t N, void* y, int y_dtype,
                             int32_t* acc_out, bool pdl, cudaStream_t s) {
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
-  auto go = [&](auto f) { return f(ctx, a, a_scale, w, w_scale, m, n, k, y, y_dtype, acc_out, pdl, s); };
-  if (M == 1) return go(launch_few<1>);
-  if (M == 2) return go(launch_few<2>);
-  if (M <= 4) return go(launch_few<4>);
-  return go(launch_few<8>);
+  if (M <= kFew) {
+    auto f = M == 1 ? launch_few<1> : launch_few<2>;
+    return f(ctx, a, a_scale, w, w_scale, n, k, y, y_dtype, acc_out, pdl, s);
+  }
+  auto f = M <= 8 ? launch_some<1> : launch_some<2>;
+  return f(ctx, a, a_scale, w, w_scale, m, n, k, y, y_dtype, acc_out, pdl, s);
 }
 
 cudaError_t launch_w8a8_codes(const int8_t* codes, __half* out, int64_t count, cudaStream_t s) {

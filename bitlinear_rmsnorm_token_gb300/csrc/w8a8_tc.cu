@@ -1,4 +1,4 @@
-// w8a8_tc.cu -- int8 x int8 contraction for 9 tokens and more on the
+// w8a8_tc.cu -- int8 x int8 contraction for 17 tokens and more on the
 // 5th-generation tensor cores.
 //
 // acc[m, n] = sum_k a[m, k] w[n, k].  sm_103a has no integer tcgen05 MMA; int8
