@@ -14,6 +14,13 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 bool known_dtype(int t) { return t == BITNET_DTYPE_F32 || t == BITNET_DTYPE_F16 || t == BITNET_DTYPE_BF16; }
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? BITNET_OK : BITNET_ERR_CUDA; }
 
+size_t size_of(int t) { return t == BITNET_DTYPE_F32 ? 4 : 2; }
+// Whether two arrays share bytes.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
 constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
 
 int check_w8_shape(int64_t M, int64_t K, int64_t N) {
@@ -89,6 +96,8 @@ int bitnet_w8a8_forward(const void* x, int x_dtype, const float* norm_w, const i
   if (rc) return rc;
   if (!aligned16(x) || !aligned16(norm_w) || !aligned16(w_codes) || !aligned4(w_scale) || !aligned16(y))
     return BITNET_ERR_MISALIGNED;
+  if (overlap(x, static_cast<size_t>(M * K) * size_of(x_dtype), y, static_cast<size_t>(M * N) * size_of(y_dtype)))
+    return BITNET_ERR_INVALID_ARG;
   DeviceContext* ctx;
   if ((rc = device_context(&ctx))) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -161,6 +170,8 @@ int bitnet_kv4_attention(const bitnet_kv4* c, const void* q, int q_dtype, int64_
     return BITNET_ERR_INVALID_ARG;
   if (num_heads > 65535) return BITNET_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(q) || !aligned16(out)) return BITNET_ERR_MISALIGNED;
+  const size_t values = static_cast<size_t>(T) * static_cast<size_t>(num_heads) * static_cast<size_t>(c->head_dim);
+  if (overlap(q, values * size_of(q_dtype), out, values * size_of(out_dtype))) return BITNET_ERR_INVALID_ARG;
   DeviceContext* ctx;
   if ((rc = device_context(&ctx))) return rc;
   int st = BITNET_OK;

@@ -125,6 +125,7 @@ struct Problem {
   float* part;    // [items + warps][rows][D + 2]: o, m, l of the segments
   int2* ends;     // [items]: first and last warp of the item
   int rows;       // rows per partial
+  int warps;      // consumer warps of the grid
 };
 
 // First key and count of the pages that sequence b's rows look at; 0 pages for
@@ -736,6 +737,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv4_join(const Problem p, O
   if (r >= n * p.G) return;
   const int2 e = p.ends[item];
   if (e.x == e.y) return;
+  if (e.x < 0 || e.y < e.x || e.y >= p.warps) return;  // never written: the launch before gave up
   const int segs = e.y - e.x + 1;
   const int64_t stride = static_cast<int64_t>(p.rows) * (D + 4);
   const float* part = p.part + (item + e.x) * stride + static_cast<int64_t>(r) * (D + 4);
@@ -808,6 +810,7 @@ cudaError_t launch_t(DeviceContext* ctx, Problem p, int64_t rows, const void* q,
     *status = BITNET_ERR_UNSUPPORTED_SHAPE;
     return cudaSuccess;
   }
+  p.warps = static_cast<int>(grid * L::kWarps);
   const size_t part = static_cast<size_t>(items + grid * L::kWarps) * p.rows * (D + 4) * 4;
   uint8_t* ws = nullptr;
   if ((*status = pool_alloc(ctx, reinterpret_cast<void**>(&ws), part + static_cast<size_t>(items) * 8, s)))

@@ -359,7 +359,8 @@ __global__ void __launch_bounds__(Layout<BN>::kThreads, 1)
 #pragma unroll
       for (int j = 0; j < L::kEpiCols; ++j) part[(half * L::kEpiCols + j) * kBM + 32 * q + lane] = acc[j];
     }
-    cluster.sync();
+    __syncwarp();
+    cluster.sync();  // (every wait before it is bounded: all CTAs of the cluster come)
     int wt, mt;
     tile_at(first, n_wt, n_mt, &wt, &mt);
     pdl_wait();
@@ -374,6 +375,7 @@ __global__ void __launch_bounds__(Layout<BN>::kThreads, 1)
       y[at] = round_out<YT>(rescale_elem(static_cast<float>(sum), __frcp_rn(a_scale[m]), __frcp_rn(__ldg(w_scale + n))));
       if (acc_out) acc_out[at] = sum;
     }
+    __syncwarp();
     cluster.sync();  // the parts stay until every CTA has read them
   }
   tc_fence_before();

@@ -328,7 +328,7 @@ BITNET_API int bitnet_quant_w8(const float* w, int64_t N, int64_t K, int8_t* w_c
  * each reciprocal and product rounded on its own, then once to y_dtype
  * (BITNET_DTYPE_F32, _F16 or _BF16).  All 256 code values are allowed; acc is
  * exact for every input (it fits int32: K <= 65536).  acc_out[M, N] int32
- * receives acc when non-NULL.  a_codes, w_codes, y, acc_out 16-byte, the scales
+ * receives acc when non-NULL.  y and acc_out share no memory with the inputs.  a_codes, w_codes, y, acc_out 16-byte, the scales
  * 4-byte aligned. */
 BITNET_API int bitnet_w8a8_gemm(const int8_t* a_codes, const float* a_scale, const int8_t* w_codes,
                                 const float* w_scale, int64_t M, int64_t K, int64_t N, void* y, int y_dtype,
@@ -336,7 +336,10 @@ BITNET_API int bitnet_w8a8_gemm(const int8_t* a_codes, const float* a_scale, con
 
 /* The projection of x: RMSNorm with norm_w, per-token int8 quantisation
  * (bitnet_rmsnorm_quant_a8 of x widened to fp32) and bitnet_w8a8_gemm of the
- * codes, bit for bit.  x[M, K] in x_dtype, norm_w[K] fp32, y[M, N] in y_dtype. */
+ * codes, bit for bit.  x[M, K] in x_dtype, norm_w[K] fp32, y[M, N] in y_dtype;
+ * x, norm_w and y 16-byte aligned.  y that shares memory with x is refused
+ * (BITNET_ERR_INVALID_ARG): few tokens are read while y is written.  From 3
+ * tokens on the codes and their scales pass through pool memory. */
 BITNET_API int bitnet_w8a8_forward(const void* x, int x_dtype, const float* norm_w, const int8_t* w_codes,
                                    const float* w_scale, int64_t M, int64_t K, int64_t N, float eps, void* y,
                                    int y_dtype, bitnet_stream_t stream);
@@ -355,17 +358,17 @@ BITNET_API int bitnet_w8a8_forward(const void* x, int x_dtype, const float* norm
  * A row of head_dim values x is stored as m = min(x), s = (max(x) - m) / 15 and
  * code = round(15 (x - m) / (max(x) - m)), ties to even, of the exact quotient; it
  * stands for code * s + m.  Rows whose range is below 1e-30 are stored as their
- * minimum (s = 0, codes 0).  A row with a non-finite value stands for
- * unspecified values; no other row is affected.
+ * minimum (s = 0, codes 0).  A row with a non-finite value, or a
+ * range beyond fp32's, stands for unspecified values; no other row is affected.
  *
  * Sequence b of a call owns the rows q_start[b] .. q_start[b + 1] - 1 of the
  * call's T new tokens; they are the last of the kv_lens[b] tokens the cache
  * holds of it, so row i of its n rows is position kv_lens[b] - n + i.  Position j
  * lies in page page_table[b * max_pages + j / 64], slot j % 64.  Rows before
  * q_start[0] and from q_start[num_seqs] on belong to no sequence, and rows of
- * negative position to no token: nothing is written for them and
- * their values change nothing (the attention output of the latter is 0).  Page-table entries of positions
- * that a call does not reach are not looked at.
+ * negative position to no token: nothing is written for them
+ * and their values change nothing (the attention output of the latter is 0).
+ * Page-table entries of positions that a call does not reach are not looked at.
  * The arrays are read on the device.  A length that the page table cannot hold
  * is cut, a page outside 0 .. num_pages - 1 is skipped (its keys count as
  * masked), and both are recorded: bitnet_last_device_status then returns
@@ -411,7 +414,8 @@ BITNET_API int bitnet_kv4_read(const bitnet_kv4* c, int64_t T, void* k, void* v,
  * q in q_dtype, out in the same type or in BITNET_DTYPE_F32; sums, softmax and
  * scores are fp32, products of q and of the probabilities with the cache's
  * integer codes exact up to 2^-22 (q or probability; 16-bit q: the
- * probabilities may be rounded to 2^-11).  scale finite. */
+ * probabilities may be rounded to 2^-11).  scale finite.  out that shares memory
+ * with q is refused (BITNET_ERR_INVALID_ARG): q is read while out is written. */
 BITNET_API int bitnet_kv4_attention(const bitnet_kv4* c, const void* q, int q_dtype, int64_t T, int32_t num_heads,
                                     int32_t max_q_len, float scale, int causal, int32_t window, void* out,
                                     int out_dtype, bitnet_stream_t stream);

@@ -64,6 +64,19 @@ def test_call_refusals():
     assert attn(out=FAKE + 8) == bn.ERR_MISALIGNED
 
 
+def test_out_over_q_is_refused():
+    L = bn.lib(build=True)
+    size = 4 * 4 * 128 * 2  # bf16 q, fp32 out: twice that
+
+    def attn(q, out, ot):
+        return L.bitnet_kv4_attention(_desc(), q, bn.DTYPE_BF16, 4, 4, 1, 0.1, 1, 0, out, ot, None)
+    for out, ot in ((FAKE, bn.DTYPE_BF16), (FAKE + size - 16, bn.DTYPE_BF16), (FAKE - size + 16, bn.DTYPE_BF16),
+                    (FAKE - 2 * size + 16, bn.DTYPE_F32)):
+        assert attn(FAKE, out, ot) == bn.ERR_INVALID_ARG
+    if not torch.cuda.is_available():  # apart: past the checks, where there is no device
+        assert attn(FAKE, FAKE + size, bn.DTYPE_BF16) not in (bn.OK, bn.ERR_INVALID_ARG)
+
+
 def test_cache_bytes():
     L = bn.lib(build=True)
     assert L.bitnet_kv4_cache_bytes(3, 2, 128) == 3 * 2 * (64 * 128 + 1024)

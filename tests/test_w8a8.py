@@ -35,6 +35,18 @@ def test_refusals():
     assert f(FAKE, 0, ODD, FAKE, FAKE, 1, 128, 1, 1e-6, FAKE, 0, None) == bn.ERR_MISALIGNED
 
 
+def test_forward_onto_its_input_is_refused():
+    L = bn.lib(build=True)
+    x, size = 1 << 20, 2 * 128 * 2
+
+    def f(y, yt):
+        return L.bitnet_w8a8_forward(x, bn.DTYPE_BF16, FAKE, FAKE, FAKE, 2, 128, 128, 1e-6, y, yt, None)
+    for y, yt in ((x, bn.DTYPE_BF16), (x + size - 16, bn.DTYPE_F32), (x - size + 16, bn.DTYPE_F16)):
+        assert f(y, yt) == bn.ERR_INVALID_ARG
+    if not torch.cuda.is_available():  # apart: past the checks, where there is no device
+        assert f(x + size, bn.DTYPE_F32) not in (bn.OK, bn.ERR_INVALID_ARG)
+
+
 def test_binding_refusals():
     z = torch.zeros
     c, w = z((2, 128), dtype=torch.int8), z((4, 128), dtype=torch.int8)
