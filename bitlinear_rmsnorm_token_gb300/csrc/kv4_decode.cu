@@ -10,6 +10,9 @@
 // the output, the others their partial sums, joined in order by a second launch
 // (no atomics: the same bits every time).
 //
+// Few items with short tables take one launch instead: a cluster of CTAs per item,
+// whose warps share its pages and join through distributed shared memory.
+//
 // A warp owns its ring of page slots; lane w of the producer warp walks warp
 // w's units, brings each page block (codes, scales and minima of 64 tokens, one
 // contiguous bulk copy) and a small descriptor into the ring, so the consumers
@@ -35,6 +38,8 @@
 // magnitude, as W is of the page's; every product and sum of integers is then
 // exact in fp32 (2^11 x 15 x 256 < 2^24).  More rows of 16-bit queries take one
 // fp16 each: the query exactly, a probability rounded by up to 2^-11.
+#include <cooperative_groups.h>
+
 #include <type_traits>
 
 #include "common.cuh"
@@ -113,6 +118,8 @@ struct Layout {
   static constexpr int offMisc = offSeq + kSeqs * 16;  // per-warp sums (two sets), abort flag
   static constexpr int kBytes = offMisc + 256;
   static_assert(kBytes <= 232448, "over the 227 KB of shared memory a CTA may use");
+  static_assert(kStages * KvBlock<D>::kBytes >= 16 * (D + 4) * 4, "a segment's sums fit the warp's ring");
+  static_assert(kSlots <= kThreads, "a thread initialises a slot's barriers");
 };
 
 struct Problem {
@@ -126,6 +133,7 @@ struct Problem {
   int2* ends;     // [items]: first and last warp of the item
   int rows;       // rows per partial
   int warps;      // consumer warps of the grid
+  int one;        // 1: a cluster of kCluster CTAs per item, joined in the launch
 };
 
 // First key and count of the pages that sequence b's rows look at; 0 pages for
@@ -145,6 +153,75 @@ __device__ __forceinline__ int seq_pages(const Problem& p, int b, int* first, in
   if (p.causal && p.window > 0) lo = max(static_cast<int64_t>(0), static_cast<int64_t>(*len) - *n - p.window + 1);
   *first = static_cast<int>(lo / kKvPage);
   return max(1, (*len + kKvPage - 1) / kKvPage - *first);
+}
+
+// CTAs that share an item in the one-launch form.
+constexpr int kCluster = 8;
+
+// A row's o (a lane's dimensions 128 i + 4 lane + c), m and l.
+template <int D>
+struct RowSum {
+  float o[D / 32], m, l;
+};
+
+// Joins `segs` segments of a row, in order, 32 segments' maxima and sums at a time;
+// part(s): where segment s keeps the row's o, m and l.
+template <int D, typename F>
+__device__ __forceinline__ RowSum<D> join_row(int segs, int lane, F part) {
+  constexpr int kPer = D / 32;
+  float o[kPer], m = -INFINITY, l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[i] = 0.0f;
+  for (int i0 = 0; i0 < segs; i0 += 32) {
+    const bool on = i0 + lane < segs;
+    const float2 ml = on ? *reinterpret_cast<const float2*>(part(i0 + lane) + D) : make_float2(-INFINITY, 0.0f);
+    float m2 = ml.x;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, k));
+    m2 = fmaxf(m, m2);
+    const float ref = m2 == -INFINITY ? 0.0f : m2;
+    const float f_old = ex2(m - ref), f = ex2(ml.x - ref);
+    m = m2;
+    float ls = f * ml.y;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, k);
+    l = l * f_old + ls;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[i] *= f_old;
+    const int most = min(32, segs - i0);
+#pragma unroll 8
+    for (int j = 0; j < most; ++j) {
+      const float fj = __shfl_sync(0xffffffffu, f, j);
+      const float4* src = reinterpret_cast<const float4*>(part(i0 + j)) + lane;
+#pragma unroll
+      for (int i = 0; i < kPer / 4; ++i) {
+        const float4 v = src[32 * i];
+        o[4 * i] = fmaf(fj, v.x, o[4 * i]);
+        o[4 * i + 1] = fmaf(fj, v.y, o[4 * i + 1]);
+        o[4 * i + 2] = fmaf(fj, v.z, o[4 * i + 2]);
+        o[4 * i + 3] = fmaf(fj, v.w, o[4 * i + 3]);
+      }
+    }
+  }
+  RowSum<D> sum;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) sum.o[i] = o[i];
+  sum.m = m;
+  sum.l = l;
+  return sum;
+}
+
+template <int D, typename OT>
+__device__ __forceinline__ void store_row(const RowSum<D>& s, int lane, OT* dst) {
+  const float inv = s.l > 0.0f ? 1.0f / s.l : (s.l == 0.0f ? 0.0f : s.l);  // no key seen: zeros; NaN stays
+#pragma unroll
+  for (int i = 0; i < D / 128; ++i) {
+    union { OT v[4]; uint2 u2; uint4 u4; } pk;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) pk.v[c] = round_out<OT>(s.o[4 * i + c] * inv);
+    if constexpr (sizeof(OT) == 4) *reinterpret_cast<uint4*>(dst + 128 * i + 4 * lane) = pk.u4;
+    else *reinterpret_cast<uint2*>(dst + 128 * i + 4 * lane) = pk.u2;
+  }
 }
 
 template <int D, int NB, bool kSplit, typename QT, typename OT, class L>
@@ -168,9 +245,14 @@ __global__ void __launch_bounds__(L::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 32);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int B_seqs = p.c.num_seqs;
+  const int B_seqs = p.one ? 0 : p.c.num_seqs;  // to divide the work over
   const unsigned H = p.c.heads;
   pdl_launch_dependents();
+  // one-launch form: the cluster's item
+  const unsigned item1 = blockIdx.x / kCluster;
+  int4 plan1 = make_int4(0, 0, 0, 0);
+  unsigned pages1 = 0;
+  if (p.one) pages1 = seq_pages(p, item1 / H, &plan1.x, &plan1.y, &plan1.z, &plan1.w);
   // ---- total work (it fits 32 bits, checked on the host), then each producer lane finds where its warp's range
   // begins: a running sum over the sequences, kSeqs of them at a time, kPer neighbours to a thread
   int4* seqs = reinterpret_cast<int4*>(smem + L::offSeq);  // first page, length, rows, first row
@@ -195,13 +277,11 @@ __global__ void __launch_bounds__(L::kThreads, 1)
       seqs[b] = v;
     }
   }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kSlots; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&ready[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    *abort_flag = 0;
+  if (threadIdx.x < L::kSlots) {
+    mbar_init(&full[threadIdx.x], 1);
+    mbar_init(&ready[threadIdx.x], 1);
+    mbar_init(&empty[threadIdx.x], 1);
+    if (threadIdx.x == 0) *abort_flag = 0;
     fence_barrier_init();
   }
   auto warp_scan = [&](unsigned x) {
@@ -224,13 +304,14 @@ __global__ void __launch_bounds__(L::kThreads, 1)
   __syncthreads();
   unsigned total = 0;
   for (int w = 0; w <= kWarps; ++w) total += misc[w];
-  const unsigned U = total * H;
+  const unsigned U = p.one ? pages1 : total * H;
+  const unsigned grid = p.one ? kCluster : gridDim.x, cta = p.one ? blockIdx.x % kCluster : blockIdx.x;
   // warp i of CTA c is number i * grid + c, so that few units spread over the CTAs; with fewer units than warps the
   // first U warps take one each.  Warp w takes uq or uq + 1 units, the first ur warps one more.
-  const unsigned W = min(gridDim.x * kWarps, U);
+  const unsigned W = min(grid * kWarps, U);
   const unsigned uq = W ? U / W : 0, ur = W ? U - uq * W : 0;
   const int my_warp = warp < kWarps ? warp : lane;  // the producer's lanes: the warp that they serve
-  const unsigned w_me = my_warp * gridDim.x + blockIdx.x;
+  const unsigned w_me = my_warp * grid + cta;
   const bool has = my_warp < kWarps && w_me < W;
   const unsigned u0 = w_me * uq + min(w_me, ur);
   const unsigned u1 = has ? u0 + uq + (w_me < ur ? 1 : 0) : 0;  // 0: nothing to do
@@ -556,7 +637,9 @@ __global__ void __launch_bounds__(L::kThreads, 1)
                   reinterpret_cast<uint4*>(dst)[i] = pk.u;
                 }
               } else {
-                float* dst = p.part + ((static_cast<int64_t>(un.item) + w_me) * p.rows + r) * (D + 4);
+                // (one-launch form: in the warp's own ring, all of whose pages have been used)
+                float* dst = p.one ? reinterpret_cast<float*>(smem + warp * kStages * B::kBytes) + r * (D + 4)
+                                   : p.part + ((static_cast<int64_t>(un.item) + w_me) * p.rows + r) * (D + 4);
 #pragma unroll
                 for (int i = 0; i < kTiles / 2; ++i)
                   reinterpret_cast<float4*>(dst + 2 * kTiles * g)[i] =
@@ -622,7 +705,17 @@ __global__ void __launch_bounds__(L::kThreads, 1)
         pages = pages_in(v);
       };
       unsigned h = 0, pg = 0, item0 = 0;  // head, page of the item, and where the item's work begins
-      if (u0 < u1) {
+      if (p.one) {
+        b = item1 / H;
+        h = item1 - b * H;
+        first = plan1.x;
+        len = plan1.y;
+        n = plan1.z;
+        q0 = plan1.w;
+        pages = pages1;
+        item0 = 0u - kItemCost;  // a page's place is its number
+        pg = u0;
+      } else if (u0 < u1) {
         open_seq();
         const unsigned o = u0 - before * H, work = pages + kItemCost;
         h = o / work;
@@ -684,7 +777,7 @@ __global__ void __launch_bounds__(L::kThreads, 1)
         } else {
           mbar_arrive(&full[slot]);
         }
-        if (pg == 0) {  // this range holds the item's first page: say which warp holds its last one
+        if (pg == 0 && !p.one) {  // this range holds the item's first page: say which warp holds its last one
           const unsigned z = at + pages - 1, wide = ur * (uq + 1);
           p.ends[un.item] = make_int2(static_cast<int>(w_me),
                                       static_cast<int>(z < wide ? z / (uq + 1) : ur + (z - wide) / uq));
@@ -716,17 +809,36 @@ __global__ void __launch_bounds__(L::kThreads, 1)
           mbar_wait(&full[lane * kStages + i % kStages], (i / kStages) & 1, p.err);
     }
   }
+  if (p.one && W > 1) {
+    // ---- the item's segments lie in the cluster's shared memory: CTA c joins rows c, c + kCluster, ...
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    __syncwarp();
+    cluster.sync();  // (every wait before it is bounded: all CTAs of the cluster come)
+    const int rows = plan1.z * p.G;
+    for (int r = cta + kCluster * warp; r < rows; r += kCluster * (kWarps + 1)) {
+      const int i_tok = r / p.G;
+      const RowSum<D> sum = join_row<D>(static_cast<int>(W), lane, [&](int i) {
+        float* own = reinterpret_cast<float*>(smem + i / kCluster * kStages * B::kBytes) + r * (D + 4);
+        return cluster.map_shared_rank(own, i % kCluster);
+      });
+      store_row<D>(sum, lane, out + (static_cast<int64_t>(plan1.w + i_tok) * p.Hq + (item1 % H) * p.G + (r - i_tok * p.G)) * D);
+    }
+    __syncwarp();
+    cluster.sync();  // the segments stay until every CTA has read them
+  }
 }
 
-// Joins the segments of the items that several warps shared, in order: a warp
-// per (item, row), 32 segments' maxima and sums at a time.
-constexpr int kJoinWarps = 4;
+// Joins the segments of the items that several warps shared, in order.  A warp per
+// (item, row), or kWide, where an item has many segments: a CTA, each of its warps a
+// part of them.
+constexpr int kJoinWarps = 8;
 
-template <int D, typename OT>
+template <int D, bool kWide, typename OT>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_kv4_join(const Problem p, OT* __restrict__ out) {
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  __shared__ __align__(16) float s_sum[kWide ? kJoinWarps : 1][D + 4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t w = kWide ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp;
   const int64_t item = w / p.rows;
   const int r = static_cast<int>(w - item * p.rows);
   if (item >= static_cast<int64_t>(p.c.num_seqs) * p.c.heads) return;
@@ -738,55 +850,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv4_join(const Problem p, O
   const int2 e = p.ends[item];
   if (e.x == e.y) return;
   if (e.x < 0 || e.y < e.x || e.y >= p.warps) return;  // never written: the launch before gave up
-  const int segs = e.y - e.x + 1;
   const int64_t stride = static_cast<int64_t>(p.rows) * (D + 4);
   const float* part = p.part + (item + e.x) * stride + static_cast<int64_t>(r) * (D + 4);
-  float o[kPer], m = -INFINITY, l = 0.0f;
+  const int segs = e.y - e.x + 1;
+  RowSum<D> sum;
+  if constexpr (kWide) {
+    const int i0 = segs * warp / kJoinWarps, i1 = segs * (warp + 1) / kJoinWarps;
+    sum = join_row<D>(i1 - i0, lane, [&](int i) { return part + (i0 + i) * stride; });
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) o[i] = 0.0f;
-  for (int i0 = 0; i0 < segs; i0 += 32) {
-    const bool on = i0 + lane < segs;
-    const float2 ml = on ? *reinterpret_cast<const float2*>(part + (i0 + lane) * stride + D)
-                         : make_float2(-INFINITY, 0.0f);
-    float m2 = ml.x;
-#pragma unroll
-    for (int k = 16; k; k >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, k));
-    m2 = fmaxf(m, m2);
-    const float ref = m2 == -INFINITY ? 0.0f : m2;
-    const float f_old = ex2(m - ref), f = ex2(ml.x - ref);
-    m = m2;
-    float ls = f * ml.y;
-#pragma unroll
-    for (int k = 16; k; k >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, k);
-    l = l * f_old + ls;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] *= f_old;
-    const int most = min(32, segs - i0);
-#pragma unroll 8
-    for (int j = 0; j < most; ++j) {
-      const float fj = __shfl_sync(0xffffffffu, f, j);
-      const float4* src = reinterpret_cast<const float4*>(part + (i0 + j) * stride) + lane;
-#pragma unroll
-      for (int i = 0; i < kPer / 4; ++i) {
-        const float4 v = src[32 * i];
-        o[4 * i] = fmaf(fj, v.x, o[4 * i]);
-        o[4 * i + 1] = fmaf(fj, v.y, o[4 * i + 1]);
-        o[4 * i + 2] = fmaf(fj, v.z, o[4 * i + 2]);
-        o[4 * i + 3] = fmaf(fj, v.w, o[4 * i + 3]);
-      }
-    }
+    for (int i = 0; i < D / 128; ++i)
+      *reinterpret_cast<float4*>(&s_sum[warp][128 * i + 4 * lane]) =
+          make_float4(sum.o[4 * i], sum.o[4 * i + 1], sum.o[4 * i + 2], sum.o[4 * i + 3]);
+    if (lane == 0) *reinterpret_cast<float2*>(&s_sum[warp][D]) = make_float2(sum.m, sum.l);
+    __syncthreads();
+    if (warp > 0) return;
+    sum = join_row<D>(kJoinWarps, lane, [&](int i) { return s_sum[i]; });
+  } else {
+    sum = join_row<D>(segs, lane, [&](int i) { return part + i * stride; });
   }
-  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // no key seen: zeros; NaN stays
   const int i_tok = r / p.G;
-  OT* dst = out + (static_cast<int64_t>(q0 + i_tok) * p.Hq + h * p.G + (r - i_tok * p.G)) * D;
-#pragma unroll
-  for (int i = 0; i < kPer / 4; ++i) {
-    union { OT v[4]; uint2 u2; uint4 u4; } pk;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) pk.v[c] = round_out<OT>(o[4 * i + c] * inv);
-    if constexpr (sizeof(OT) == 4) *reinterpret_cast<uint4*>(dst + 128 * i + 4 * lane) = pk.u4;
-    else *reinterpret_cast<uint2*>(dst + 128 * i + 4 * lane) = pk.u2;
-  }
+  store_row<D>(sum, lane, out + (static_cast<int64_t>(q0 + i_tok) * p.Hq + h * p.G + (r - i_tok * p.G)) * D);
 }
 
 // Warps and ring slots: as many page blocks as shared memory holds, and the
@@ -796,6 +879,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv4_join(const Problem p, O
 template <int D, int NB>
 using LayoutOf =
     std::conditional_t<D == 128, std::conditional_t<NB == 1, Layout<128, 11, 2>, Layout<128, 7, 3>>, Layout<256, 6, 2>>;
+
+// The join takes a CTA a row from this many segments an item on (average): one query
+// token, 8 kv heads of 128, 16384 tokens (200 segments): 49 us with a warp a row, 22
+// with a CTA.
+constexpr int64_t kWideSegs = 16;
+// The one-launch form's most items (15 clusters of 8 do not fit the GPU at once) and
+// most pages of the page table a warp.  One query token, 8 kv heads of 128, against
+// two launches: 1021 tokens 7.4 / 9.7 us, 4096 10.7 / 11.5, 16384 18.1 / 21.9, 32768
+// 25.4 / 23.8, and 3 us less for a call (no second launch, no workspace); one head of
+// 256: 1021 tokens 9.0 / 10.3, 4096 14.4 / 11.9.
+constexpr int64_t kOneItems = 14;
+template <int D>
+constexpr int kOnePagesWarp = D == 128 ? 4 : 1;
 
 template <int D, int NB, bool kSplit, typename QT, typename OT>
 cudaError_t launch_t(DeviceContext* ctx, Problem p, int64_t rows, const void* q, void* out, cudaStream_t s,
@@ -810,6 +906,25 @@ cudaError_t launch_t(DeviceContext* ctx, Problem p, int64_t rows, const void* q,
     *status = BITNET_ERR_UNSUPPORTED_SHAPE;
     return cudaSuccess;
   }
+  auto kern = k_kv4_decode<D, NB, kSplit, QT, OT, L>;
+  cudaError_t e = allow_smem(ctx, reinterpret_cast<const void*>(kern), L::kBytes);
+  if (e != cudaSuccess) return e;
+  if (items <= kOneItems && p.c.max_pages <= kOnePagesWarp<D> * kCluster * L::kWarps) {
+    p.one = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(items * kCluster));
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = L::kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<const Problem>(p), static_cast<const QT*>(q), static_cast<OT*>(out));
+  }
   p.warps = static_cast<int>(grid * L::kWarps);
   const size_t part = static_cast<size_t>(items + grid * L::kWarps) * p.rows * (D + 4) * 4;
   uint8_t* ws = nullptr;
@@ -817,16 +932,15 @@ cudaError_t launch_t(DeviceContext* ctx, Problem p, int64_t rows, const void* q,
     return cudaSuccess;
   p.part = reinterpret_cast<float*>(ws);
   p.ends = reinterpret_cast<int2*>(ws + part);
-  auto kern = k_kv4_decode<D, NB, kSplit, QT, OT, L>;
-  cudaError_t e = allow_smem(ctx, reinterpret_cast<const void*>(kern), L::kBytes);
-  if (e == cudaSuccess) {
+  {
     kern<<<static_cast<unsigned>(grid), L::kThreads, L::kBytes, s>>>(p, static_cast<const QT*>(q),
                                                                      static_cast<OT*>(out));
     e = cudaGetLastError();
   }
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((items * p.rows + kJoinWarps - 1) / kJoinWarps));
+    const bool wide = grid * L::kWarps > kWideSegs * items;  // more segments an item, on average
+    cfg.gridDim = dim3(static_cast<unsigned>(wide ? items * p.rows : (items * p.rows + kJoinWarps - 1) / kJoinWarps));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -834,7 +948,8 @@ cudaError_t launch_t(DeviceContext* ctx, Problem p, int64_t rows, const void* q,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_kv4_join<D, OT>, static_cast<const Problem>(p), static_cast<OT*>(out));
+    e = cudaLaunchKernelEx(&cfg, wide ? k_kv4_join<D, true, OT> : k_kv4_join<D, false, OT>,
+                           static_cast<const Problem>(p), static_cast<OT*>(out));
   }
   pool_free(ws, s);
   return e;

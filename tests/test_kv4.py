@@ -291,6 +291,27 @@ def test_few_tokens(device, D, Hkv, G, dtype, n):
 
 
 @gpu
+@pytest.mark.parametrize("most", [None, 400])  # a long page table takes two launches
+@pytest.mark.parametrize("D,Hkv,G,n,dtype", [(128, 7, 2, 1, BF16), (128, 8, 1, 1, F32), (128, 1, 4, 4, F16), (128, 2, 8, 1, F32),
+                                             (256, 1, 4, 2, BF16), (256, 1, 2, 1, F32), (256, 3, 8, 1, F16)])
+def test_few_items(device, D, Hkv, G, n, dtype, most):
+    """Few (sequence, kv head) pairs: one launch, or two with a row's many parts joined by a CTA.  Lengths from none to
+    more pages than the warps that share them, a window, pages outside the cache."""
+    for lens, window in (([0, 65], 0), ([6100, n], 0), ([2900, 513], 300)):
+        c = ref.Case(41, [n] * 2, lens, Hkv, D, most=most)
+        check(c, queries(42, c.T, Hkv * G, D, dtype), G, window=window, what=f"{lens}")
+    c = ref.Case(43, [n], [3000], Hkv, D, most=most)
+    c.table[0, [2, 3, 40]] = [-1, 1 << 30, c.cache.shape[0]]
+    q = queries(44, n, Hkv * G, D, dtype)
+    got = run_attention(c, c.dev(), q, G)
+    assert bn.last_device_status() == bn.ERR_BAD_INDEX
+    c.table[0, [2, 3, 40]] = 0  # any page: the formula leaves them out
+    want, bound = ref.attention(c, q.float().numpy(), D ** -0.5, skip_pages=(2, 3, 40))
+    err = np.abs(got.float().cpu().numpy().astype(np.float64) - want)
+    assert (err <= ref.bound_for(c, want, bound, dtype, got.dtype)).all()
+
+
+@gpu
 @pytest.mark.parametrize("D,Hkv,G", [(128, 2, 2), (256, 1, 4), (128, 1, 7)])
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("causal", [True, False])
