@@ -25,6 +25,12 @@
 //   8 epilogue warps: quadrant, half of the tile's tokens each
 //   a warp for the TMA of raw weights (128 rows x 128 bytes, 128B swizzle), one
 //   for the token codes', and an issuer per pipeline
+// Measured: 16384 tokens, K = 4096, N = 16384: 1.6 ms, 1.37 PFLOP/s (0.70 of a bf16
+// library product), the tensor cores 63% busy: with BN = 192 a K block of 128 takes
+// 1024 cycles of shared memory (tokens read by the MMAs, weights in and out) for 768
+// of MMA.  2047 tokens, K = 4096, N = 8192, norm and bf16 in and out: 125 us, 1.1
+// PFLOP/s (704 tiles on 152 SMs: five rounds for the work of 4.6).  64 tokens,
+// 8192 x 8192: 24.5 us (2.7 TB/s of weights).
 // Few tiles (short or narrow problems): a cluster of S CTAs takes a tile, each a
 // range of K, and adds the parts up through distributed shared memory (int32:
 // the order does not matter).
