@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kWarps = 8;
 // Tokens up to which dp4a and mma.sync take the product.  Two tokens, dp4a against
-// mma.sync: 2048 x 2048 3.1 / 3.7 us, 4096 x 4096 6.3 / 6.4, 8192 x 8192 16.5 / 15.0.
+// mma.sync: 2048 x 2048 3.1 / 3.7 us, 4096 x 4096 6.3 / 6.4, 8192 x 8192 16.5 / 13.7.
 constexpr int64_t kFew = 2, kSome = 16;
 
 // The one-launch form's most tokens, and longest row (its codes stay in 32 KB of
@@ -309,18 +309,21 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 // products, K in an order of its own that the tokens' bytes follow.  The fp32 sums
 // take kFold chunks (at most 512 of K: at most 2^23, exact) and then join the warp's
 // int32 sums in shared memory, where the warps' meet in the end.
-// 13 tokens, 8192 x 8192: 19 us with the weights out of L2 (3.5 TB/s), 4096 x 4096:
-// 7.4 us, against 21 and 11.8 us of the tcgen05 kernel, whose 128-channel tiles,
-// TMEM operand and cluster exchange pay from more tokens on (24 tokens: 22 us
-// against 39); 8 tokens 15 and 6.4 us, where dp4a took 37 and 10.4.  Chunks dealt to
-// the warps one by one (64 bytes of a row at a time) cost 22 us, 16 channels a
-// CTA 21 us, four chunks ahead (spills) 21 us.
+// 13 tokens, 8192 x 8192: 16.9 us with the weights out of L2 (4.0 TB/s), 4096 x
+// 4096: 7.4 us, against 21 and 11.8 us of the tcgen05 kernel, whose 128-channel
+// tiles, TMEM operand and cluster exchange pay from more tokens on (24 tokens: 22 us
+// against 39); 8 tokens 13.7 (4.9 TB/s) and 6.1 us, where dp4a took 37 and 10.4.
+// Latency of both streams: three chunks of weights and one of codes ahead 18.7 us,
+// 4 and 2 (spills) 21, three CTAs an SM (spills) 24; chunks dealt to the warps one
+// by one (64 bytes of a row at a time) 22, 16 channels a CTA 21.
 template <int kNB, int kTiles, int kW>
 __global__ void __launch_bounds__(kW * 32, 16 / kW)
     k_w8a8_some(const int8_t* __restrict__ a, const float* __restrict__ a_scale, const int8_t* __restrict__ w,
                 const float* __restrict__ w_scale, int M, int N, int K, void* __restrict__ y, int y_dtype,
                 int32_t* __restrict__ acc_out) {
-  constexpr int kAhead = kTiles == 1 ? 8 : 3, kFold = kTiles == 1 ? 8 : 6, kRows = 16 * kTiles, kCols = 8 * kNB;
+  constexpr int kAhead = kTiles == 1 ? 8 : 2, kFold = 8;     // chunks of weights in flight, of an fp32 sum
+  constexpr int kRing = kTiles == 1 && kNB == 1 ? 4 : 2;     // chunks of the tokens' codes in flight
+  constexpr int kRows = 16 * kTiles, kCols = 8 * kNB;
   __shared__ int s_part[kW][kCols][kRows + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * kRows;
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW)
 #pragma unroll
   for (int b = 0; b < kNB; ++b)
     ar[b] = reinterpret_cast<const uint4*>(a + static_cast<int64_t>(min(8 * b + g, M - 1)) * K) + 16 * warp + t;
-  uint4 wv[kAhead][2 * kTiles], av[kNB];
+  uint4 wv[kAhead][2 * kTiles], av[kRing][kNB];
   auto fetch = [&](int i, int c) {
 #pragma unroll
     for (int r = 0; r < 2 * kTiles; ++r) wv[i][r] = ld_stream(wr[r] + at(c));
@@ -344,10 +347,12 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW)
   for (int i = 0; i < kAhead; ++i)
     if (i < mine) fetch(i, i);
   pdl_wait();  // the codes come from the launch before this one
-  if (mine > 0) {
 #pragma unroll
-    for (int b = 0; b < kNB; ++b) av[b] = *ar[b];
-  }
+  for (int i = 0; i < kRing; ++i)
+    if (i < mine) {
+#pragma unroll
+      for (int b = 0; b < kNB; ++b) av[i][b] = ar[b][at(i)];
+    }
   float acc[kTiles][kNB][4];
   auto fold = [&](bool first) {
 #pragma unroll
@@ -370,11 +375,11 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW)
       uint32_t bl[kNB][4], bh[kNB][4];
 #pragma unroll
       for (int b = 0; b < kNB; ++b) {
-        int8_to_h2(av[b].x, bl[b][0], bh[b][0]);
-        int8_to_h2(av[b].y, bl[b][1], bh[b][1]);
-        int8_to_h2(av[b].z, bl[b][2], bh[b][2]);
-        int8_to_h2(av[b].w, bl[b][3], bh[b][3]);
-        if (c + 1 < mine) av[b] = ar[b][at(c + 1)];
+        int8_to_h2(av[i % kRing][b].x, bl[b][0], bh[b][0]);
+        int8_to_h2(av[i % kRing][b].y, bl[b][1], bh[b][1]);
+        int8_to_h2(av[i % kRing][b].z, bl[b][2], bh[b][2]);
+        int8_to_h2(av[i % kRing][b].w, bl[b][3], bh[b][3]);
+        if (c + kRing < mine) av[i % kRing][b] = ar[b][at(c + kRing)];
       }
 #pragma unroll
       for (int r = 0; r < kTiles; ++r) {
