@@ -71,7 +71,7 @@ struct Layout {
   static constexpr int kRawWarp = kUnpackWarps + kEpiWarps, kTokWarp = kRawWarp + 1, kMmaWarp0 = kRawWarp + 2;
   static constexpr int kThreads = 32 * (kMmaWarp0 + kPipes);
   static constexpr int kTokStage = BN * 256;           // 128 of K: two 64-wide swizzled slabs
-  static constexpr int kTok = BN == 192 ? 3 : (BN == 128 ? 4 : (BN == 64 ? 5 : 8));
+  static constexpr int kTok = BN == 192 ? 3 : (BN == 128 ? 4 : (BN == 64 ? 6 : 8));
   static constexpr int kRaw = BN == 192 ? 4 : (BN == 128 ? 5 : 8);
   static constexpr int kACol0 = 2 * kPipes * BN;       // accumulators [pipe][2], then the A stages
   static constexpr int kAPer = (kTmemCols - kACol0) / kAStageCols / kPipes;  // A stages of a pipeline
@@ -85,6 +85,10 @@ struct Layout {
   static constexpr int kBytes = offMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAPer >= 2, "TMEM columns");
+  // a pipeline has slots of its own: whoever waits for a slot has waited for its phase before, so that a wait's parity
+  // cannot mean the phase before that (loads may land out of order)
+  static constexpr int kTokPer = kTok / kPipes, kRawPer = kRaw / kPipes;
+  static_assert(kTok % kPipes == 0 && kRaw % kPipes == 0, "ring slots are shared out evenly");
   static_assert(kAlloc <= 232448, "over the 227 KB of shared memory a CTA may use");
   static_assert(kTok * kTokStage + kRaw * kRawBytes >= BN * kBM * 4, "the split's exchange reuses the rings");
 };
@@ -160,37 +164,47 @@ __global__ void __launch_bounds__(Layout<BN>::kThreads, 1)
 
   int32_t acc[L::kEpiCols];  // epilogue: this thread's channel, its warp's tokens
 
-  // Block kb of a tile is running number g0 + kb (raw and token rings); pipeline j takes the tile's blocks j, j + kP, ..
+  // Pipeline j takes a tile's blocks j, j + kP, ..; its n-th block of all is in its slots n % kRawPer, n % kTokPer
   if (warp == L::kRawWarp) {
     // ------------------------------------------------------------ raw weights
     // (not written by the launch before this one: no wait for it)
     if (lane == 0) {
-      int i = 0;
+      int n[kP] = {};
       for (int t = first; t < tiles; t += step) {
         int wt, mt;
         tile_at(t, n_wt, n_mt, &wt, &mt);
-        for (int kb = kb0; kb < kb1; ++kb, ++i) {
-          const int s = i % L::kRaw;
-          if (!mbar_wait(&raw_empty[s], ((i / L::kRaw) & 1) ^ 1, err, abort_flag)) goto raw_done;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          const int j = (kb - kb0) % kP, i = j ? n[kP - 1]++ : n[0]++;
+          const int s = L::kRawPer * j + i % L::kRawPer;
+          if (!mbar_wait(&raw_empty[s], ((i / L::kRawPer) & 1) ^ 1, err, abort_flag)) {
+            --n[j ? kP - 1 : 0];
+            goto raw_done;
+          }
           mbar_arrive_expect_tx(&raw_full[s], kRawBytes);
           tma_load_2d(smem + L::offRaw + s * kRawBytes, &tm_w, kb * 128, wt * kBM, &raw_full[s]);
         }
       }
     raw_done:
       if (*abort_flag)  // given up: copies in flight must land before the CTA's shared memory goes
-        for (int k = max(0, i - L::kRaw); k < i; ++k) mbar_wait(&raw_full[k % L::kRaw], (k / L::kRaw) & 1, err);
+        for (int j = 0; j < kP; ++j)
+          for (int k = max(0, n[j] - L::kRawPer); k < n[j]; ++k)
+            mbar_wait(&raw_full[L::kRawPer * j + k % L::kRawPer], (k / L::kRawPer) & 1, err);
     }
   } else if (warp == L::kTokWarp) {
     // ------------------------------------------------------------ token codes
     if (lane == 0) {
       pdl_wait();
-      int i = 0;
+      int n[kP] = {};
       for (int t = first; t < tiles; t += step) {
         int wt, mt;
         tile_at(t, n_wt, n_mt, &wt, &mt);
-        for (int kb = kb0; kb < kb1; ++kb, ++i) {
-          const int s = i % L::kTok;
-          if (!mbar_wait(&tok_empty[s], ((i / L::kTok) & 1) ^ 1, err, abort_flag)) goto tok_done;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          const int j = (kb - kb0) % kP, i = j ? n[kP - 1]++ : n[0]++;
+          const int s = L::kTokPer * j + i % L::kTokPer;
+          if (!mbar_wait(&tok_empty[s], ((i / L::kTokPer) & 1) ^ 1, err, abort_flag)) {
+            --n[j ? kP - 1 : 0];
+            goto tok_done;
+          }
           mbar_arrive_expect_tx(&tok_full[s], L::kTokStage);
           uint8_t* dst = smem + L::offTok + s * L::kTokStage;
           tma_load_2d(dst, &tm_tok, kb * 128, mt * BN, &tok_full[s]);
@@ -199,22 +213,24 @@ __global__ void __launch_bounds__(Layout<BN>::kThreads, 1)
       }
     tok_done:
       if (*abort_flag)
-        for (int k = max(0, i - L::kTok); k < i; ++k) mbar_wait(&tok_full[k % L::kTok], (k / L::kTok) & 1, err);
+        for (int j = 0; j < kP; ++j)
+          for (int k = max(0, n[j] - L::kTokPer); k < n[j]; ++k)
+            mbar_wait(&tok_full[L::kTokPer * j + k % L::kTokPer], (k / L::kTokPer) & 1, err);
     }
   } else if (warp >= L::kMmaWarp0) {
     // ------------------------------------------------------------ MMA issue
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_f16_f32(kBM, BN);
       const int j = warp - L::kMmaWarp0;
-      int n = 0, c = 0, g0 = 0;  // running stages and chunks of the pipeline, blocks of the CTA
-      for (int t = first; t < tiles; t += step, g0 += blocks) {
+      int n = 0, c = 0;  // running blocks and chunks of the pipeline
+      for (int t = first; t < tiles; t += step) {
         for (int kb = j, in = 0; kb < blocks; kb += kP, ++n) {
           const uint32_t d = tmem + static_cast<uint32_t>((2 * j + (c & 1)) * BN);
           if (in == 0) {
             if (!mbar_wait(&acc_empty[2 * j + (c & 1)], ((c >> 1) & 1) ^ 1, err, abort_flag)) goto mma_done;
             tc_fence_after();
           }
-          const int as = L::kAPer * j + n % L::kAPer, s = (g0 + kb) % L::kTok;
+          const int as = L::kAPer * j + n % L::kAPer, s = L::kTokPer * j + n % L::kTokPer;
           if (!mbar_wait(&a_full[as], (n / L::kAPer) & 1, err, abort_flag)) goto mma_done;  // the tokens, too
           tc_fence_after();
           const uint64_t bd = sw128_kmajor_desc(smem_u32(smem + L::offTok + s * L::kTokStage));
@@ -245,22 +261,23 @@ __global__ void __launch_bounds__(Layout<BN>::kThreads, 1)
     // ------------------------------------------------------------ unpack
     const int j = warp >> 2, q = warp & 3, row = 32 * q + lane;
     const uint32_t tq = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(L::kACol0);
-    int n = 0, g0 = 0;
-    int pending = -1;  // running block whose stores are under way and not yet announced
+    int n = 0;             // running blocks of the pipeline
+    bool pending = false;  // the stores of block n - 1 are under way and not yet announced
     auto announce = [&]() {
       tmem_st_wait();
       tc_fence_before();
-      const bool ok = mbar_wait(&tok_full[pending % L::kTok], (pending / L::kTok) & 1, err, abort_flag);
+      const bool ok = mbar_wait(&tok_full[L::kTokPer * j + (n - 1) % L::kTokPer], ((n - 1) / L::kTokPer) & 1, err, abort_flag);
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&a_full[L::kAPer * j + (n - 1) % L::kAPer]);
-      pending = -1;
+      pending = false;
       return ok;
     };
-    for (int t = first; t < tiles; t += step, g0 += blocks) {
+    for (int t = first; t < tiles; t += step) {
       for (int kb = j; kb < blocks; kb += kP) {
-        const int g = g0 + kb, rs = g % L::kRaw;
-        if (pending >= 0 && !mbar_test(&raw_full[rs], (g / L::kRaw) & 1) && !announce()) goto unpack_done;
-        if (!mbar_wait(&raw_full[rs], (g / L::kRaw) & 1, err, abort_flag)) goto unpack_done;
+        const int rs = L::kRawPer * j + n % L::kRawPer;
+        const unsigned rp = (n / L::kRawPer) & 1;
+        if (pending && !mbar_test(&raw_full[rs], rp) && !announce()) goto unpack_done;
+        if (!mbar_wait(&raw_full[rs], rp, err, abort_flag)) goto unpack_done;
         const uint8_t* src = smem + L::offRaw + rs * kRawBytes + row * 128;
         const int as = L::kAPer * j + n % L::kAPer;
 #pragma unroll
@@ -276,7 +293,7 @@ __global__ void __launch_bounds__(Layout<BN>::kThreads, 1)
           }
           if (h == 0) {
             // announce the stage before, whose stores ran during this decode
-            if (pending >= 0 && !announce()) goto unpack_done;
+            if (pending && !announce()) goto unpack_done;
             if (!mbar_wait(&a_empty[as], ((n / L::kAPer) & 1) ^ 1, err, abort_flag)) goto unpack_done;
             tc_fence_after();
           } else {  // the slot's bytes are in registers
@@ -287,11 +304,11 @@ __global__ void __launch_bounds__(Layout<BN>::kThreads, 1)
           __syncwarp();
           tmem_st_32x32b_x32(tq + static_cast<uint32_t>(as * kAStageCols + 32 * h), cols);
         }
-        pending = g;
+        pending = true;
         ++n;
       }
     }
-    if (pending >= 0) announce();
+    if (pending) announce();
   unpack_done:;
   } else {
     // ------------------------------------------------------------ epilogue

@@ -156,6 +156,25 @@ def test_gemm_of_some_tokens(device, M, K, N):
 
 
 @gpu
+@pytest.mark.parametrize("M,N", [(700, 1), (30, 300), (60, 300), (500, 130)])
+def test_gemm_again_and_again(device, M, N):
+    """Long rows split over clusters, many times from cold operands: loads that land late or out of order change nothing."""
+    K = 16640
+    a, w = (torch.from_numpy(codes(s, (n, K), "any")).cuda() for s, n in ((3, M), (4, N)))
+    sa, sw = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    # float64 products of int8 codes and their sums (below 2^53) are exact, in any order
+    want = (a.cpu().numpy().astype(np.float64) @ w.cpu().numpy().astype(np.float64).T).astype(np.int64)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    accs = [torch.empty((M, N), dtype=torch.int32, device="cuda") for _ in range(150)]
+    for i, acc in enumerate(accs):
+        if i % 3 == 0:
+            flush.fill_(i & 1)
+        bn.w8a8_gemm(a, sa, w, sw, acc_out=acc)
+    want = torch.from_numpy(want).cuda()
+    assert all(torch.equal(acc.long(), want) for acc in accs)
+
+
+@gpu
 @pytest.mark.parametrize("M", [1, 5, 8, 9, 40, 100])
 @pytest.mark.parametrize("K,N", [(640, 96), (4096, 264)])
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
