@@ -18,7 +18,7 @@
 // A stage is 128 of K (a raw slot): the issuing thread pays some 240 cycles for a
 // wait behind MMAs in flight and 45 per instruction, so it waits once per 8 MMAs
 // (stages of 64 and two waits: 740 cycles per 64 of K whatever BN).  Narrow
-// tiles, whose MMAs are short, run two pipelines (unpack warps, issuer,
+// tiles, whose MMAs are short, run two pipelines (ring slots, unpack warps, issuer,
 // accumulators), every other stage each.
 //   4 unpack warps per pipeline: lane quadrant q, one weight row a thread; they
 //               also wait for the stage's tokens, so that the issuer has one wait
