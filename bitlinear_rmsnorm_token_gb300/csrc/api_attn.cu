@@ -75,7 +75,7 @@ int bitnet_w8a8_gemm(const int8_t* a_codes, const float* a_scale, const int8_t* 
   DeviceContext* ctx;
   if ((rc = device_context(&ctx))) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (w8a8_few_supported(M))
+  if (w8a8_few_supported(M, K, N))
     return cuda_status(launch_w8a8_few(ctx, a_codes, a_scale, w_codes, w_scale, M, K, N, y, y_dtype, acc_out, false, s));
   __half* f16 = nullptr;
   if ((rc = pool_alloc(ctx, reinterpret_cast<void**>(&f16), static_cast<size_t>(M * K) * 2, s))) return rc;
@@ -103,7 +103,7 @@ int bitnet_w8a8_forward(const void* x, int x_dtype, const float* norm_w, const i
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (w8a8_forward_few_supported(M, K))
     return cuda_status(launch_w8a8_forward_few(ctx, x, x_dtype, norm_w, eps, w_codes, w_scale, M, K, N, y, y_dtype, s));
-  const bool few = w8a8_few_supported(M);
+  const bool few = w8a8_few_supported(M, K, N);
   const size_t code_bytes = (static_cast<size_t>(M * K) * (few ? 1 : 2) + 255) & ~size_t(255);
   uint8_t* ws = nullptr;
   if ((rc = pool_alloc(ctx, reinterpret_cast<void**>(&ws), code_bytes + static_cast<size_t>(M) * 4, s))) return rc;

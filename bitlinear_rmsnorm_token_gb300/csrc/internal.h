@@ -178,7 +178,7 @@ bool w8a8_forward_few_supported(int64_t M, int64_t K);
 cudaError_t launch_w8a8_forward_few(const DeviceContext* ctx, const void* x, int x_dtype, const float* g, float eps,
                                     const int8_t* w, const float* w_scale, int64_t M, int64_t K, int64_t N, void* y,
                                     int y_dtype, cudaStream_t s);
-bool w8a8_few_supported(int64_t M);
+bool w8a8_few_supported(int64_t M, int64_t K, int64_t N);
 cudaError_t launch_w8a8_few(const DeviceContext* ctx, const int8_t* a, const float* a_scale, const int8_t* w,
                             const float* w_scale, int64_t M, int64_t K, int64_t N, void* y, int y_dtype,
                             int32_t* acc_out, bool pdl, cudaStream_t s);

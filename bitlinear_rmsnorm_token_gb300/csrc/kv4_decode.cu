@@ -893,7 +893,7 @@ using LayoutOf =
 // token, 8 kv heads of 128, 16384 tokens (200 segments): 49 us with a warp a row, 22
 // with a CTA.
 constexpr int64_t kWideSegs = 16;
-// The one-launch form's most items (15 clusters of 8 do not fit the GPU at once) and
+// The one-launch form's most items (16 clusters of 8 do not fit the GPU at once) and
 // most pages of the page table a warp.  One query token, 8 kv heads of 128, against
 // two launches: 1021 tokens 7.4 / 9.7 us, 4096 10.7 / 11.5, 16384 18.1 / 21.9, 32768
 // 25.4 / 23.8, and 3 us less for a call (no second launch, no workspace); one head of

@@ -8,8 +8,8 @@
 // warp streams kR rows of them with 16-byte loads, many in flight, and multiplies
 // with dp4a (4 products an instruction and token) against the codes, which stay in
 // L1.  3 to 16: the weights still go straight to registers, but into mma.sync with
-// the tokens as its 8 columns.  The first loads of a warp are issued before the wait
-// for the launch that writes the codes.  From 17 tokens on tcgen05 (w8a8_tc.cu).
+// the tokens as its 8 columns (up to 32 tokens where the weights are few).  The first loads of a warp are issued before the wait
+// for the launch that writes the codes.  More tokens on tcgen05 (w8a8_tc.cu).
 // One token, 4096 x 4096: 5.5 us with the weights out of L2; 8192 x 8192: 13.7 us
 // (4.9 TB/s).
 #include <type_traits>
@@ -25,6 +25,10 @@ constexpr int kWarps = 8;
 // Tokens up to which dp4a and mma.sync take the product.  Two tokens, dp4a against
 // mma.sync: 2048 x 2048 3.1 / 3.7 us, 4096 x 4096 6.3 / 6.4, 8192 x 8192 16.5 / 13.7.
 constexpr int64_t kFew = 2, kSome = 16;
+// Weights up to which mma.sync takes 17 to 32 tokens, too.  24 tokens, mma.sync
+// against tcgen05: 1024 x 1024 4.2 / 8.0 us, 2048 x 2048 5.1 / 9.3, 4096 x 4096
+// 9.9 / 12.4, but 4096 x 14336 24 / 20.
+constexpr int64_t kSomeWeights = 1 << 24;
 
 // The one-launch form's most tokens, and longest row (its codes stay in 32 KB of
 // shared memory, its fixed-point sums in their range).  Against two launches, per
@@ -321,8 +325,8 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW)
     k_w8a8_some(const int8_t* __restrict__ a, const float* __restrict__ a_scale, const int8_t* __restrict__ w,
                 const float* __restrict__ w_scale, int M, int N, int K, void* __restrict__ y, int y_dtype,
                 int32_t* __restrict__ acc_out) {
-  constexpr int kAhead = kTiles == 1 ? 8 : 2, kFold = 8;     // chunks of weights in flight, of an fp32 sum
-  constexpr int kRing = kTiles == 1 && kNB == 1 ? 4 : 2;     // chunks of the tokens' codes in flight
+  constexpr int kAhead = kTiles == 1 && kNB < 4 ? 8 : 2, kFold = 8;     // chunks of weights in flight, of an fp32 sum
+  constexpr int kRing = kNB == 4 ? 1 : (kTiles == 1 && kNB == 1 ? 4 : 2);   // chunks of the tokens' codes in flight
   constexpr int kRows = 16 * kTiles, kCols = 8 * kNB;
   __shared__ int s_part[kW][kCols][kRows + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -418,7 +422,8 @@ cudaError_t launch_some(const DeviceContext* ctx, const int8_t* a, const float* 
                         const float* w_scale, int M, int N, int K, void* y, int y_dtype, int32_t* acc_out, bool pdl,
                         cudaStream_t s) {
   // 32 channels a CTA if that leaves every SM one; 4 warps a CTA if 8 would be more than the SMs hold at a time
-  const bool wide = N >= 32 * ctx->num_sms, many = N > 64 * ctx->num_sms;
+  // (32 tokens' operands leave registers for 16)
+  const bool wide = kNB < 4 && N >= 32 * ctx->num_sms, many = kNB < 4 && N > 64 * ctx->num_sms;
   const int rows = wide ? 32 : 16;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(N) + rows - 1) / rows));
@@ -429,7 +434,10 @@ cudaError_t launch_some(const DeviceContext* ctx, const int8_t* a, const float* 
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kern = many ? k_w8a8_some<kNB, 2, 4> : (wide ? k_w8a8_some<kNB, 2, 8> : k_w8a8_some<kNB, 1, 8>);
+  auto kern = k_w8a8_some<kNB, 1, 8>;
+  if constexpr (kNB < 4) {
+    if (wide) kern = many ? k_w8a8_some<kNB, 2, 4> : k_w8a8_some<kNB, 2, 8>;
+  }
   return cudaLaunchKernelEx(&cfg, kern, a, a_scale, w, w_scale, M, N, K, y, y_dtype, acc_out);
 }
 
@@ -512,7 +520,9 @@ cudaError_t launch_w8a8_forward_few(const DeviceContext* ctx, const void* x, int
   }
 }
 
-bool w8a8_few_supported(int64_t M) { return M <= kSome; }
+bool w8a8_few_supported(int64_t M, int64_t K, int64_t N) {
+  return M <= kSome || (M <= 32 && N * K <= kSomeWeights);
+}
 
 cudaError_t launch_w8a8_few(const DeviceContext* ctx, const int8_t* a, const float* a_scale, const int8_t* w,
                             const float* w_scale, int64_t M, int64_t K, int64_t N, void* y, int y_dtype,
@@ -522,7 +532,7 @@ cudaError_t launch_w8a8_few(const DeviceContext* ctx, const int8_t* a, const flo
     auto f = M == 1 ? launch_few<1> : launch_few<2>;
     return f(ctx, a, a_scale, w, w_scale, n, k, y, y_dtype, acc_out, pdl, s);
   }
-  auto f = M <= 8 ? launch_some<1> : launch_some<2>;
+  auto f = M <= 8 ? launch_some<1> : (M <= 16 ? launch_some<2> : launch_some<4>);
   return f(ctx, a, a_scale, w, w_scale, m, n, k, y, y_dtype, acc_out, pdl, s);
 }
 

@@ -38,7 +38,10 @@
 // unwinds without trapping.
 #include <cooperative_groups.h>
 
+#include <map>
+#include <mutex>
 #include <type_traits>
+#include <utility>
 
 #include "common.cuh"
 #include "internal.h"
@@ -475,6 +478,38 @@ cudaError_t launch_bn(const DeviceContext* ctx, EncodeTiledFn encode, const __ha
 struct Plan {
   int bn, S;
 };
+// Clusters of S CTAs that the device holds at a time: a cluster stays within a group
+// of SMs (152 SMs hold 76 of 2, 36 of 4, 15 of 8).  One cluster more is a second
+// wave: 40 tokens, 2048 x 2048 as 16 clusters of 8 15.7 us, as 16 of 4 10.0 us.
+int clusters_at_once(const DeviceContext* ctx, int S) {
+  static std::mutex mu;
+  static std::map<std::pair<int, int>, int> known;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto it = known.find({ctx->device, S});
+  if (it != known.end()) return it->second;
+  const void* kern = reinterpret_cast<const void*>(k_w8a8_tc<64, float>);
+  int n = 0;
+  if (allow_smem(ctx, kern, Layout<64>::kAlloc) == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctx->num_sms / S * S));
+    cfg.blockDim = dim3(Layout<64>::kThreads);
+    cfg.dynamicSmemBytes = Layout<64>::kAlloc;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+  }
+  known[{ctx->device, S}] = n;
+  return n;
+}
+
 Plan make_plan(const DeviceContext* ctx, int64_t M, int64_t K, int64_t N) {
   Plan best = {192, 1};
   int64_t best_cost = INT64_MAX;
@@ -482,7 +517,8 @@ Plan make_plan(const DeviceContext* ctx, int64_t M, int64_t K, int64_t N) {
   for (int bn : {16, 32, 64, 128, 192}) {
     const int64_t tiles = ((M + bn - 1) / bn) * ((N + kBM - 1) / kBM);
     for (int S : {1, 2, 4, 8}) {
-      if (S > nkb || (S > 1 && tiles * S > ctx->num_sms)) continue;  // a split takes one wave
+      // a split takes one wave
+      if (S > nkb || (S > 1 && (tiles * S > ctx->num_sms || tiles > clusters_at_once(ctx, S)))) continue;
       const int64_t rounds = (tiles * S + ctx->num_sms - 1) / ctx->num_sms;
       const int64_t pipes = bn <= 64 ? 380 : 740;
       const int64_t per_kb = 4 * bn + 256 > pipes ? 4 * bn + 256 : pipes;

@@ -148,8 +148,8 @@ def test_quant_w8(device, N, K):
 
 
 @gpu
-@pytest.mark.parametrize("M", [2, 3, 8, 9, 16, 17])
-@pytest.mark.parametrize("K,N", [(128, 4999), (384, 9801), (2176, 9801), (4224, 4999)])
+@pytest.mark.parametrize("M", [2, 3, 8, 9, 16, 17, 25, 32])
+@pytest.mark.parametrize("K,N", [(128, 4999), (384, 9801), (2176, 9801), (4224, 4999), (4096, 4097), (16384, 1000)])
 def test_gemm_of_some_tokens(device, M, K, N):
     """The widths at which a CTA takes more channels or fewer warps, with row lengths that leave warps without a part."""
     check_gemm(M, K, N, acc=True)
